@@ -443,6 +443,92 @@ qlora_status nf4_layer_error_rank_noalloc(int32_t n_layers, const uint16_t* cons
                                           int32_t w_dtype, nf4_qconfig q, int32_t K,
                                           double* err, int32_t* order, uint8_t* keep, qlora_stream_t stream);
 
+/* --------------------------------- between the linears, and 8-bit linears
+ *
+ * The RMS norm of the residual stream, linears whose activations are 8 bit too
+ * ("FALQON: Accelerating LoRA Fine-tuning with Low-Bit Floating-Point
+ * Arithmetic" summary page: a frozen base in low-bit floating point), and the
+ * linears of a mixture of experts.
+ *
+ * e4m3 blocks: a block's a = max(max|x|, 2^-100), scale = fp32(a / 448), codes
+ * = e4m3 (OCP, 448 the largest) of the real quotient 448 x / a, nearest, ties to
+ * even; the value a code stands for is code * scale. A block that holds a NaN or
+ * an infinity gets NaN codes. Rows (activations, output gradients) have a scale
+ * for each 1 x 128 block, [M][ceil(in / 128)]; weights for each 128 x 128 block,
+ * [experts][ceil(out / 128)][ceil(in / 128)]; the last blocks may be short.
+ *
+ * `in` and `out` are multiples of 16 up to 2^24, M is 1 .. 2^30, any value in
+ * between. These calls use a workspace only where they take one; calls on
+ * several streams may share a status workspace (qlora_expert_workspace_size()
+ * bytes: the status word alone, zeroed once). */
+
+/* h = bf16(x + residual) (x where residual is NULL; h may be NULL then),
+ * rstd = 1 / sqrt(mean(h^2) + eps) per row (fp32 [M]), y = h rstd weight, as bf16
+ * (y), as e4m3 codes with scales (y_codes, y_scale; quantized from the fp32
+ * value), or both; at least one. weight: bf16 or fp32 [H]. H % 8 == 0, H <= 32768.
+ * h may be x or residual itself. */
+qlora_status qlora_rms_norm_fwd(const uint16_t* x, const uint16_t* residual, const void* weight, int32_t w_dtype,
+                                int64_t M, int64_t H, float eps, uint16_t* h, uint16_t* y, uint8_t* y_codes,
+                                float* y_scale, float* rstd, qlora_stream_t stream);
+
+/* Gradients of the above (of y as if it were not rounded to 8 bit): with
+ * g = dy weight, dx = dh + rstd (g - h rstd^2 mean(g h)), the gradient of x and of
+ * the residual alike; dh (may be NULL) is the gradient that reaches h itself.
+ * dw (may be NULL; fp32 [H]) = sum over rows of dy h rstd, the same bits from run
+ * to run. The workspace (scratch only, no status word, not shared by calls that
+ * overlap) is needed with dw. */
+size_t qlora_rms_norm_bwd_workspace_size(int64_t M, int64_t H);
+qlora_status qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const float* rstd,
+                                const void* weight, int32_t w_dtype, int64_t M, int64_t H, uint16_t* dx, float* dw,
+                                void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/* e4m3 codes and scales of bf16 rows X [M x in]. */
+qlora_status fp8_quantize_rows(const uint16_t* X, int64_t M, int64_t in, uint8_t* codes, float* scale,
+                               qlora_stream_t stream);
+/* e4m3 codes and scales of a weight (bf16 or fp32) [experts][out x in]. A
+ * non-finite weight sets QLORA_ERR_NONFINITE in the status word. */
+qlora_status fp8_quantize_weight(const void* W, int32_t w_dtype, int64_t experts, int64_t out, int64_t in,
+                                 uint8_t* codes, float* scale, void* workspace, size_t workspace_bytes,
+                                 qlora_stream_t stream);
+
+/* Descriptor of a weight, or of the stacked weights of up to 1024 experts, each
+ * out x in: e4m3 codes with block scales, or bf16. */
+typedef struct {
+  int64_t experts;
+  int64_t out;
+  int64_t in;
+  int32_t is_bf16;
+  const uint8_t* codes;     /* e4m3 [experts][out][in]                      (is_bf16 = 0) */
+  const float* scale;       /* fp32 [experts][ceil(out/128)][ceil(in/128)] (is_bf16 = 0) */
+  const uint16_t* w_bf16;   /* bf16 [experts][out][in]                     (is_bf16 = 1) */
+} qlora_expert_weight;
+
+size_t qlora_expert_workspace_size(void);
+
+/* Linear with an e4m3 weight (experts = 1) and e4m3 rows, products summed in fp32:
+ * Y [M x out] = X W^T, and for the backward of the frozen weight dX [M x in] = dY W. */
+qlora_status fp8_linear_fwd(const qlora_expert_weight* w, const uint8_t* x_codes, const float* x_scale, int64_t M,
+                            uint16_t* Y, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+qlora_status fp8_linear_bwd(const qlora_expert_weight* w, const uint8_t* dy_codes, const float* dy_scale, int64_t M,
+                            uint16_t* dX, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/* Linear grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of X, sorted by
+ * expert, go through expert e: Y_e = X_e W_e^T, dX_e = dY_e W_e (dX may be NULL)
+ * and dW_e = dY_e^T X_e (fp32 [experts][out x in], zero for an expert without
+ * rows; may be NULL; bf16 weights only). X and dY are bf16 for a bf16 weight,
+ * e4m3 codes with scales for an e4m3 weight; the X of the backward (needed for
+ * dW) is bf16.
+ * offsets: int32 [experts + 1] in device memory, ascending, within 0 .. M. Rows
+ * before offsets[0] and from offsets[experts] on are not written. Offsets that
+ * descend or leave 0 .. M set QLORA_ERR_SHAPE in the status word and are taken as
+ * the running maximum of their values clamped to 0 .. M. */
+qlora_status qlora_grouped_linear_fwd(const qlora_expert_weight* w, const void* X, const float* x_scale, int64_t M,
+                                      const int32_t* offsets, uint16_t* Y, void* workspace, size_t workspace_bytes,
+                                      qlora_stream_t stream);
+qlora_status qlora_grouped_linear_bwd(const qlora_expert_weight* w, const uint16_t* X, const void* dY,
+                                      const float* dy_scale, int64_t M, const int32_t* offsets, uint16_t* dX,
+                                      float* dW, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,11 @@ class QLoraWeight(ctypes.Structure):
                 ("w_bf16", c_void_p)]
 
 
+class ExpertWeight(ctypes.Structure):
+    _fields_ = [("experts", c_int64), ("out", c_int64), ("in_", c_int64), ("is_bf16", c_int32), ("codes", c_void_p),
+                ("scale", c_void_p), ("w_bf16", c_void_p)]
+
+
 # name -> (restype, argtypes); every symbol declared in include/qlora_b200.h
 SIGNATURES = {
     "qlora_status_str": (c_char_p, [c_int]),
@@ -77,6 +82,23 @@ SIGNATURES = {
     "nf4_quantize_error_rank": (c_int, [c_int32, POINTER(c_void_p), POINTER(c_int64), c_int32, NF4QConfig, c_int32,
                                         POINTER(c_void_p), POINTER(c_void_p), POINTER(c_void_p), POINTER(c_void_p),
                                         c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qlora_rms_norm_fwd": (c_int, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_float, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "qlora_rms_norm_bwd_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "qlora_rms_norm_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "fp8_quantize_rows": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "fp8_quantize_weight": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                    c_size_t, c_void_p]),
+    "qlora_expert_workspace_size": (c_size_t, []),
+    "fp8_linear_fwd": (c_int, [POINTER(ExpertWeight), c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_size_t,
+                               c_void_p]),
+    "fp8_linear_bwd": (c_int, [POINTER(ExpertWeight), c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_size_t,
+                               c_void_p]),
+    "qlora_grouped_linear_fwd": (c_int, [POINTER(ExpertWeight), c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                                         c_void_p, c_size_t, c_void_p]),
+    "qlora_grouped_linear_bwd": (c_int, [POINTER(ExpertWeight), c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None

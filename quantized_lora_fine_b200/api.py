@@ -8,6 +8,16 @@ step runs in libqlora_b200.so. Functions mirror the C entry points:
     linear_fwd(w, X, L1, L2, scale)        -> (Y, T)           (qlora_linear_fwd)
     linear_bwd(w, X, dY, L1, L2, scale, T) -> (dX, dL1, dL2)   (qlora_linear_bwd)
     layer_error_rank(Ws, K, double_quant)  -> (err, order, keep) (nf4_layer_error_rank)
+
+Between the linears, 8-bit linears, and linears grouped by expert:
+
+    rms_norm_fwd(x, weight, eps, residual, fp8)       -> (y, h, rstd)   (qlora_rms_norm_fwd)
+    rms_norm_bwd(dy, h, rstd, weight, dh)             -> (dx, dw)       (qlora_rms_norm_bwd)
+    fp8_quantize_rows(X)                              -> FP8Rows        (fp8_quantize_rows)
+    fp8_quantize_weight(W)                            -> FP8Weight      (fp8_quantize_weight)
+    fp8_linear_fwd(w, X), fp8_linear_bwd(w, dY)       -> Y, dX          (fp8_linear_fwd, fp8_linear_bwd)
+    grouped_linear_fwd(W, X, offsets)                 -> Y              (qlora_grouped_linear_fwd)
+    grouped_linear_bwd(W, X, dY, offsets)             -> (dX, dW)       (qlora_grouped_linear_bwd)
 """
 from __future__ import annotations
 
@@ -54,6 +64,20 @@ class Workspace:
         if buf is None or buf.numel() < nbytes:
             buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
             cls._bufs[key] = buf
+        return buf
+
+    @classmethod
+    def status_word(cls, index: int) -> torch.Tensor:
+        """The status word of the calls that need no other workspace, one per device:
+        calls on any stream, and captured ones, may share it."""
+        buf = cls._bufs.get((index, None))
+        if buf is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("make one 8-bit or grouped call on this device before capturing one: the first "
+                                   "call sets up the device's status word")
+            buf = torch.zeros(256, dtype=torch.uint8, device=torch.device("cuda", index))
+            torch.cuda.current_stream(index).synchronize()
+            cls._bufs[(index, None)] = buf
         return buf
 
     @classmethod
@@ -396,6 +420,305 @@ def rank_errors(err: torch.Tensor, K: int):
     keep = torch.empty(L, dtype=torch.uint8, device=err.device)
     check(lib.nf4_rank_errors(L, _ptr(err), int(K), _ptr(order), _ptr(keep), _stream()), "nf4_rank_errors")
     return order, keep
+
+
+# ------------------------------------------------------------------ norm, 8-bit and grouped linears
+
+_F8 = torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+class _On:
+    """Makes `device` current for a call and gives its current stream; every tensor of the
+    call must be there."""
+    __slots__ = ("index", "prev")
+
+    def __init__(self, device: torch.device, *tensors: Optional[torch.Tensor]):
+        for t in tensors:
+            if t is not None and t.device != device:
+                raise ValueError(f"every tensor of a call must be on one device: got {device} and {t.device}")
+        self.index = device.index
+
+    def __enter__(self) -> int:
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.index:
+            torch.cuda.set_device(self.index)
+        return torch.cuda.current_stream(self.index).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev != self.index:
+            torch.cuda.set_device(self.prev)
+
+
+def _need_shape(t: torch.Tensor, shape: Tuple[int, ...], name: str):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _need_rows(t: torch.Tensor, name: str):
+    _need(t, torch.bfloat16, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
+
+
+def _out(t: Optional[torch.Tensor], shape: Tuple[int, ...], dtype, device, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name)
+    _need_shape(t, shape, name)
+    return t
+
+
+@dataclasses.dataclass
+class FP8Rows:
+    """Rows in e4m3: codes float8_e4m3fn [M, in], scale fp32 [M, ceil(in / 128)]; a value
+    is its code times its block's scale."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    def __post_init__(self):
+        _need(self.codes, _F8, "codes")
+        _need(self.scale, torch.float32, "scale")
+        if self.codes.dim() != 2:
+            raise ValueError("codes must be 2-D")
+        _need_shape(self.scale, (self.codes.shape[0], _blocks(self.codes.shape[1])), "scale")
+
+
+@dataclasses.dataclass
+class FP8Weight:
+    """A frozen weight in e4m3, stored out x in: codes float8_e4m3fn [out, in], or
+    [experts, out, in], with a scale for each 128 x 128 block, fp32
+    [(experts,) ceil(out / 128), ceil(in / 128)]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    def __post_init__(self):
+        _need(self.codes, _F8, "codes")
+        _need(self.scale, torch.float32, "scale")
+        if self.codes.dim() not in (2, 3):
+            raise ValueError("codes must be [out, in] or [experts, out, in]")
+        o, i = self.codes.shape[-2:]
+        _need_shape(self.scale, tuple(self.codes.shape[:-2]) + (_blocks(o), _blocks(i)), "scale")
+
+    @property
+    def out(self) -> int:
+        return self.codes.shape[-2]
+
+    @property
+    def inp(self) -> int:
+        return self.codes.shape[-1]
+
+
+def _expert_weight(W) -> Tuple[_lib.ExpertWeight, int, int, int]:
+    """(descriptor, experts, out, in) of an FP8Weight or a bf16 tensor [(experts,) out, in]."""
+    s = _lib.ExpertWeight()
+    if isinstance(W, FP8Weight):
+        t = W.codes
+        s.codes, s.scale = t.data_ptr(), W.scale.data_ptr()
+    else:
+        t = W
+        _need(t, torch.bfloat16, "W")
+        if t.dim() not in (2, 3):
+            raise ValueError("W must be [out, in] or [experts, out, in]")
+        s.is_bf16, s.w_bf16 = 1, t.data_ptr()
+    s.experts = t.shape[0] if t.dim() == 3 else 1
+    s.out, s.in_ = t.shape[-2], t.shape[-1]
+    return s, s.experts, s.out, s.in_
+
+
+def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                 fp8: bool = False):
+    """(y, h, rstd): h = bf16(x + residual) (x itself without a residual), rstd = 1 /
+    sqrt(mean(h^2) + eps) per row, y = h rstd weight. y is bf16, or FP8Rows with fp8=True
+    (quantized from the fp32 value). x: bf16 [M, H] with H % 8 == 0; weight: bf16 or fp32 [H]."""
+    _need_rows(x, "x")
+    M, H = x.shape
+    if weight.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("weight must be bf16 or fp32")
+    _need(weight, weight.dtype, "weight")
+    _need_shape(weight, (H,), "weight")
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual")
+        _need_shape(residual, (M, H), "residual")
+    dev = x.device
+    lib = _lib.load()
+    with _On(dev, weight, residual) as stream:
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        h = x if residual is None else torch.empty_like(x)
+        if fp8:
+            q = FP8Rows(torch.empty((M, H), dtype=_F8, device=dev),
+                        torch.empty((M, _blocks(H)), dtype=torch.float32, device=dev))
+            y, y8, ys = None, q.codes.data_ptr(), q.scale.data_ptr()
+        else:
+            y, y8, ys = torch.empty_like(x), None, None
+        check(lib.qlora_rms_norm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(),
+                                     DTYPE_BF16 if weight.dtype == torch.bfloat16 else DTYPE_F32, M, H, float(eps),
+                                     None if residual is None else h.data_ptr(), _ptr(y), y8, ys, rstd.data_ptr(),
+                                     stream), "qlora_rms_norm_fwd")
+    return (q if fp8 else y), h, rstd
+
+
+def rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                 dh: Optional[torch.Tensor] = None, need_dw: bool = True):
+    """(dx, dw) from the gradient of y and, with dh, the one that reaches h itself: dx (bf16) is
+    the gradient of x and of the residual alike, dw (fp32 [H]; None with need_dw=False) the
+    weight's. h and rstd are rms_norm_fwd's. An 8-bit y counts as not rounded."""
+    _need_rows(dy, "dy")
+    M, H = dy.shape
+    for t, nm in ((h, "h"), (dh, "dh")):
+        if t is not None:
+            _need(t, torch.bfloat16, nm)
+            _need_shape(t, (M, H), nm)
+    _need(rstd, torch.float32, "rstd")
+    _need_shape(rstd, (M,), "rstd")
+    if weight.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("weight must be bf16 or fp32")
+    _need(weight, weight.dtype, "weight")
+    _need_shape(weight, (H,), "weight")
+    dev = dy.device
+    lib = _lib.load()
+    with _On(dev, h, rstd, weight, dh) as stream:
+        dx = torch.empty_like(dy)
+        dw = torch.empty(H, dtype=torch.float32, device=dev) if need_dw else None
+        nbytes = lib.qlora_rms_norm_bwd_workspace_size(M, H) if need_dw else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None   # this call's alone
+        check(lib.qlora_rms_norm_bwd(dy.data_ptr(), _ptr(dh), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(),
+                                     DTYPE_BF16 if weight.dtype == torch.bfloat16 else DTYPE_F32, M, H,
+                                     dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, stream), "qlora_rms_norm_bwd")
+    return dx, dw
+
+
+def fp8_quantize_rows(X: torch.Tensor) -> FP8Rows:
+    """e4m3 codes of bf16 rows [M, in] with a scale for each 128 values (in % 16 == 0)."""
+    _need_rows(X, "X")
+    M, inp = X.shape
+    lib = _lib.load()
+    with _On(X.device) as stream:
+        q = FP8Rows(torch.empty((M, inp), dtype=_F8, device=X.device),
+                    torch.empty((M, _blocks(inp)), dtype=torch.float32, device=X.device))
+        check(lib.fp8_quantize_rows(X.data_ptr(), M, inp, q.codes.data_ptr(), q.scale.data_ptr(), stream),
+              "fp8_quantize_rows")
+    return q
+
+
+def fp8_quantize_weight(W: torch.Tensor) -> FP8Weight:
+    """e4m3 codes of a bf16 or fp32 weight [out, in] or [experts, out, in] with a scale for each
+    128 x 128 block. A non-finite weight is reported by status()."""
+    if W.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("W must be bf16 or fp32")
+    _need(W, W.dtype, "W")
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be [out, in] or [experts, out, in]")
+    o, i = W.shape[-2:]
+    lib = _lib.load()
+    with _On(W.device) as stream:
+        ws = Workspace.status_word(W.device.index)
+        w = FP8Weight(torch.empty(W.shape, dtype=_F8, device=W.device),
+                      torch.empty(tuple(W.shape[:-2]) + (_blocks(o), _blocks(i)), dtype=torch.float32,
+                                  device=W.device))
+        check(lib.fp8_quantize_weight(W.data_ptr(), DTYPE_BF16 if W.dtype == torch.bfloat16 else DTYPE_F32,
+                                      W.shape[0] if W.dim() == 3 else 1, o, i, w.codes.data_ptr(), w.scale.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), stream), "fp8_quantize_weight")
+    return w
+
+
+def _fp8_linear(fn: str, w: FP8Weight, rows, cols_in: int, cols_out: int, out: Optional[torch.Tensor], name: str):
+    if not isinstance(w, FP8Weight) or w.codes.dim() != 2:
+        raise ValueError("w must be an FP8Weight [out, in]")
+    if not isinstance(rows, FP8Rows):
+        rows = fp8_quantize_rows(rows)
+    M = rows.codes.shape[0]
+    _need_shape(rows.codes, (M, cols_in), name)
+    dev = rows.codes.device
+    cs = _expert_weight(w)[0]
+    lib = _lib.load()
+    with _On(dev, rows.scale, w.codes, w.scale, out) as stream:
+        ws = Workspace.status_word(dev.index)
+        out = _out(out, (M, cols_out), torch.bfloat16, dev, "out")
+        check(getattr(lib, fn)(ctypes.byref(cs), rows.codes.data_ptr(), rows.scale.data_ptr(), M, out.data_ptr(),
+                               ws.data_ptr(), ws.numel(), stream), fn)
+    return out
+
+
+def fp8_linear_fwd(w: FP8Weight, X, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W^T (bf16 [M, out]) with e4m3 weight and rows. X: FP8Rows, or bf16 [M, in], which is
+    quantized first."""
+    return _fp8_linear("fp8_linear_fwd", w, X, w.inp, w.out, Y, "X")
+
+
+def fp8_linear_bwd(w: FP8Weight, dY, dX: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX = dY W (bf16 [M, in]), the gradient through the frozen weight. dY: FP8Rows, or bf16
+    [M, out], which is quantized first."""
+    return _fp8_linear("fp8_linear_bwd", w, dY, w.out, w.inp, dX, "dY")
+
+
+def _grouped_rows(W, rows, cols: int, name: str):
+    """(tensor, scale or None) of a grouped call's rows in the weight's kind."""
+    if isinstance(W, FP8Weight):
+        if not isinstance(rows, FP8Rows):
+            rows = fp8_quantize_rows(rows)
+        t, sc = rows.codes, rows.scale
+    else:
+        _need_rows(rows, name)
+        t, sc = rows, None
+    _need_shape(t, (t.shape[0], cols), name)
+    return t, sc
+
+
+def _need_offsets(offsets: torch.Tensor, E: int):
+    _need(offsets, torch.int32, "offsets")
+    _need_shape(offsets, (E + 1,), "offsets")
+
+
+def grouped_linear_fwd(W, X, offsets: torch.Tensor, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y (bf16 [M, out]): rows offsets[e]:offsets[e + 1] of X go through expert e, Y_e = X_e W_e^T.
+    W: bf16 [experts, out, in] with bf16 X [M, in], or an FP8Weight with FP8Rows (bf16 X is
+    quantized first). offsets: int32 [experts + 1] on the device, ascending within 0 .. M; rows
+    outside every group are not written (pass Y to keep what is in them)."""
+    cs, E, o, i = _expert_weight(W)
+    _need_offsets(offsets, E)
+    x, sx = _grouped_rows(W, X, i, "X")
+    M, dev = x.shape[0], x.device
+    lib = _lib.load()
+    with _On(dev, sx, W.codes if sx is not None else W, offsets, Y) as stream:
+        ws = Workspace.status_word(dev.index)
+        Y = _out(Y, (M, o), torch.bfloat16, dev, "Y")
+        check(lib.qlora_grouped_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), M, offsets.data_ptr(),
+                                           Y.data_ptr(), ws.data_ptr(), ws.numel(), stream),
+              "qlora_grouped_linear_fwd")
+    return Y
+
+
+def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, need_dX: bool = True,
+                       need_dW: bool = True, dX: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None):
+    """(dX, dW) of grouped_linear_fwd: dX_e = dY_e W_e (bf16 [M, in]; rows outside every group are
+    not written) and dW_e = dY_e^T X_e (fp32 [experts, out, in], zero for an expert without rows;
+    bf16 weights only: an FP8Weight is frozen, pass need_dW=False). X may be None without dW."""
+    cs, E, o, i = _expert_weight(W)
+    _need_offsets(offsets, E)
+    if not need_dX and not need_dW:
+        raise ValueError("need_dX or need_dW must be true")
+    if need_dW and isinstance(W, FP8Weight):
+        raise ValueError("an FP8Weight is frozen: pass need_dW=False")
+    dy, sy = _grouped_rows(W, dY, o, "dY")
+    M, dev = dy.shape[0], dy.device
+    if need_dW:
+        if X is None:
+            raise ValueError("X is needed for dW")
+        _need_rows(X, "X")
+        _need_shape(X, (M, i), "X")
+    lib = _lib.load()
+    with _On(dev, sy, W.codes if sy is not None else W, offsets, X if need_dW else None, dX, dW) as stream:
+        ws = Workspace.status_word(dev.index)
+        dX = _out(dX, (M, i), torch.bfloat16, dev, "dX") if need_dX else None
+        dW = _out(dW, (E, o, i), torch.float32, dev, "dW") if need_dW else None
+        check(lib.qlora_grouped_linear_bwd(ctypes.byref(cs), _ptr(X) if need_dW else None, dy.data_ptr(), _ptr(sy), M,
+                                           offsets.data_ptr(), _ptr(dX), _ptr(dW), ws.data_ptr(), ws.numel(), stream),
+              "qlora_grouped_linear_bwd")
+    return dX, dW
 
 
 def status() -> int:

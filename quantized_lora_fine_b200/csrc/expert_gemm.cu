@@ -1,0 +1,671 @@
+// Products whose rows are grouped by expert, in bf16 and in block-scaled e4m3, on
+// tcgen05 (a dense 8-bit linear is the case of one group).
+//
+//   Fwd  Y_e  = X_e W_e^T        Dx  dX_e = dY_e W_e        Dw  dW_e = dY_e^T X_e
+//
+// with X_e the rows [offsets[e], offsets[e + 1]) of X. In e4m3 every 128 values of a
+// row share a scale and every 128 x 128 block of W shares one, so with k running
+// over blocks of 128
+//
+//   Y[m, n] = sum_k sa[m, k] sb[n / 128, k] (sum_{j in block k} qa[m, j] qb[n, j]).
+//
+// The inner sums run on the tensor cores, 128 values deep, into a fresh TMEM buffer
+// for each k; the outer sum is one fp32 multiply-add per value in the registers of
+// the epilogue warps, which read buffer k while the tensor cores fill buffer k + 1.
+// In bf16 the tensor cores sum over all of K and the epilogue reads once per tile.
+//
+// One persistent CTA per SM, or one CTA pair per two SMs (cta_group::2, tiles of 256 x
+// 256: each CTA stages its 128 rows of A and its 128 columns of B, so a byte from L2
+// feeds twice the products that it does in a 128 x 128 tile). Roles:
+//   warp 0      TMA producer
+//   warp 1      TMEM allocation, MMA issue (even CTA of a pair)
+//   warps 2..   epilogue, 4 lane quadrants x (tile columns / 64): each warp owns 32
+//               rows x 64 columns, in registers
+// Stage: 128 rows (or columns) x 128 bytes of K for each operand, 128-byte swizzle,
+// K-major as stored along K, MN-major where the reduction runs over rows.
+//
+// Groups end where they end: A rows past a group's last row are loaded (or left as
+// they were in shared memory) and multiplied, and never stored; products of rows are
+// independent, so they cannot reach a stored one. B's tensor map has the expert as its
+// third dimension, so columns of A past K meet zeros and not the next expert's rows.
+// In Dw the rows are summed over, so the last step of a group is cleared in shared
+// memory past the group's last row in both operands (a zero in one only would let a
+// NaN of another expert's row through).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+
+#include "expert_gemm.cuh"
+#include "gemm.cuh"
+#include "internal.cuh"
+#include "nf4_device.cuh"
+#include "ptx.cuh"
+
+namespace qlb {
+
+namespace {
+
+struct ExpertParams {
+  int M, E;
+  int n_cols;            // columns of D
+  int tiles_n;           // ceil(n_cols / BN)
+  int tiles_r;           // Dw: row tiles of D per expert
+  int nk;                // K steps (Fwd, Dx)
+  int d_rows;            // Dw: rows of D per expert
+  int a_box;             // rows of A per TMA box: 128, or 32 where groups are small
+  const int32_t* offsets;
+  const float* sa;
+  const float* sb;
+  int nb_a;              // scales per row of A
+  int nb_n;              // column blocks of sb (clamps the ragged last tile)
+  int64_t sb_e, sb_n, sb_k;   // strides of sb: expert, column block, K block
+  uint16_t* d;
+  int64_t ld_d;
+  int* status;
+};
+
+template <bool PAIR_, bool F8_, ExpertMode MODE_>
+struct ExpertCfg {
+  static constexpr bool PAIR = PAIR_, F8 = F8_;
+  static constexpr ExpertMode MODE = MODE_;
+  static constexpr bool DW = MODE == ExpertMode::Dw;
+  static constexpr bool A_MN = DW, B_MN = MODE != ExpertMode::Fwd;
+  static constexpr int BM = PAIR ? 256 : 128, BN = PAIR ? 256 : 128;
+  static constexpr int kElem = F8 ? 1 : 2;
+  static constexpr int BK = 128 / kElem;                // K per step: 128 bytes
+  static constexpr int kChunk = 128 / kElem;            // MN-major: columns per 128-byte row
+  static constexpr int kA = 128 * 128, kB = 128 * 128;  // bytes per CTA and stage
+  static constexpr int kStage = kA + kB;
+  static constexpr int STAGES = PAIR ? 4 : 5;
+  static constexpr int kColGroups = BN / 64;
+  static constexpr int kEpiWarps = 4 * kColGroups;
+  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kStaging = kEpiWarps * 4096;     // 32 rows x 128 bytes per warp
+  static constexpr int kBarOff = STAGES * kStage + kStaging;
+  static constexpr int kNumBars = 2 * STAGES + 6;
+  static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
+  static constexpr int kSmem = kTableOff + 2 * (kMaxExperts + 1) * 4 + 1024;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// acc += v * s for two values at once.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s2) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s2));
+}
+__device__ __forceinline__ uint64_t dup2(float s) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t a, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(a));
+}
+
+struct ExpertTile {
+  int e, n0, nk;
+  int row0, rows;     // Fwd, Dx: first row of the tile in A and D, rows of the group from there
+                      // Dw: first row of D in the expert, rows of D from there
+  int k_row0, k_rows; // Dw: the group's rows
+};
+
+// Tiles run over an expert's row tiles first, then its column tiles, then the experts:
+// a column tile of the weight is shared by neighbours in time. `e` only moves up.
+template <class C>
+__device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, const int* starts, const int* tiles, int t,
+                                                  int& e) {
+  ExpertTile x;
+  if constexpr (C::DW) {
+    const int per = p.tiles_r * p.tiles_n;
+    e = t / per;
+    const int r = t - e * per;
+    const int n = r / p.tiles_r;
+    x.row0 = (r - n * p.tiles_r) * C::BM;
+    x.rows = p.d_rows - x.row0;
+    x.n0 = n * C::BN;
+    x.k_row0 = starts[e];
+    x.k_rows = starts[e + 1] - starts[e];
+    x.nk = (x.k_rows + C::BK - 1) / C::BK;
+  } else {
+    const int v = t / p.tiles_n;
+    while (tiles[e + 1] <= v) ++e;
+    const int mt = tiles[e + 1] - tiles[e];
+    const int r = t - tiles[e] * p.tiles_n;
+    const int n = r / mt;
+    const int m = r - n * mt;
+    x.row0 = starts[e] + m * C::BM;
+    x.rows = starts[e + 1] - x.row0;
+    x.n0 = n * C::BN;
+    x.nk = p.nk;
+    x.k_row0 = x.k_rows = 0;
+  }
+  x.e = e;
+  return x;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmD, const ExpertParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bars = base + C::kBarOff;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
+  auto tfull_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
+  auto tempty_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
+  const uint32_t tail_bar = bars + 8u * (2 * C::STAGES + 4);
+  const uint32_t drain_bar = bars + 8u * (2 * C::STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kNumBars);
+  int* starts = reinterpret_cast<int*>(smem + C::kTableOff);
+  int* tiles = starts + kMaxExperts + 1;
+
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = C::PAIR ? cluster_ctarank() : 0u;
+  const int unit = C::PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
+  const int units = C::PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full_bar(s), C::PAIR ? 2 : 1);   // one arrival per CTA's producer
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), (C::PAIR ? 2 : 1) * C::kEpiWarps);
+    }
+    mbar_init(tail_bar, 1);
+    mbar_init(drain_bar, 1);
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    if constexpr (C::PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  pdl_wait();
+  pdl_launch();
+  // Group table: starts[e] is the running maximum of the offsets clamped to [0, M] (so
+  // whatever they hold, groups lie inside A and do not overlap), tiles[e] the row tiles
+  // of the groups before e.
+  if (warp == 0) {
+    if (p.offsets == nullptr) {
+      if (lane == 0) {
+        starts[0] = 0;
+        starts[1] = p.M;
+        tiles[0] = 0;
+        tiles[1] = (p.M + C::BM - 1) / C::BM;
+      }
+    } else {
+      int run = 0, sum = 0, prev = 0;
+      bool bad = false;
+      for (int i0 = 0; i0 <= p.E; i0 += 32) {
+        const int i = i0 + int(lane);
+        const int raw = i <= p.E ? __ldg(p.offsets + i) : 0;
+        const int c = min(max(raw, 0), p.M);
+        int v = max(c, run);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, v, d);
+          if (int(lane) >= d) v = max(v, u);
+        }
+        if (i <= p.E && (raw != c || v != c)) bad = true;
+        int before = __shfl_up_sync(0xffffffffu, v, 1);
+        if (lane == 0) before = prev;
+        // row tiles of group i - 1, which ends at v
+        int n = (i >= 1 && i <= p.E) ? (v - before + C::BM - 1) / C::BM : 0;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, n, d);
+          if (int(lane) >= d) n += u;
+        }
+        if (i <= p.E) {
+          starts[i] = v;
+          tiles[i] = sum + n;
+        }
+        run = prev = __shfl_sync(0xffffffffu, v, 31);
+        sum += __shfl_sync(0xffffffffu, n, 31);
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) set_status_site(p.status, QLORA_ERR_SHAPE, 60);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (C::PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int num_tiles = C::DW ? p.E * p.tiles_r * p.tiles_n : tiles[p.E] * p.tiles_n;
+  constexpr uint64_t kDrainNs = 100000000ull;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+    }
+    uint32_t it = 0, ntail = 0;
+    int e = 0;
+    bool ok = true;
+    for (int t = unit; t < num_tiles && ok; t += units) {
+      const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
+      const int a_rows = min(128, max(0, x.rows - int(rank) * 128));
+      const int boxes = C::A_MN || C::PAIR ? 1 : (a_rows + p.a_box - 1) / p.a_box;
+      const int b0 = x.n0 + int(rank) * 128;        // this CTA's columns of B
+      const int a0 = x.row0 + int(rank) * 128;      // this CTA's rows of D
+      for (int kb = 0; kb < x.nk; ++kb, ++it) {
+        const int s = it % C::STAGES;
+        const uint32_t ph = (it / C::STAGES) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph ^ 1u))) {
+          if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 61);
+          ok = false;
+          break;
+        }
+        const uint32_t a_s = base + s * C::kStage, b_s = a_s + C::kA;
+        const int valid = C::DW ? x.k_rows - kb * C::BK : C::BK;   // rows of the reduction in this step
+        const bool tail = C::DW && valid < C::BK;
+        if (lane == 0) {
+          uint32_t bar;
+          if (tail) {
+            bar = tail_bar;
+            mbar_arrive_expect_tx(bar, C::kStage);
+          } else if constexpr (C::PAIR) {
+            // The even CTA's barrier counts both CTAs' bytes.
+            bar = mapa_shared(full_bar(s), 0);
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * C::kStage);
+            else mbar_arrive_cluster(bar);
+          } else {
+            bar = full_bar(s);
+            mbar_arrive_expect_tx(bar, (C::A_MN ? C::kA : boxes * p.a_box * 128) + C::kB);
+          }
+          const int k0 = kb * C::BK;
+          auto load2 = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy) {
+            if (C::PAIR && !tail) tma_load_2d_pair(dst, m, bar, cx, cy);
+            else tma_load_2d(dst, m, bar, cx, cy);
+          };
+          auto load3 = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy) {
+            if (C::PAIR && !tail) tma_load_3d_pair(dst, m, bar, cx, cy, x.e);
+            else tma_load_3d(dst, m, bar, cx, cy, x.e);
+          };
+          if constexpr (C::DW) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              load2(a_s + c * 8192, &tmA, a0 + 64 * c, x.k_row0 + k0);
+              load2(b_s + c * 8192, &tmB, b0 + 64 * c, x.k_row0 + k0);
+            }
+          } else {
+            for (int b = 0; b < boxes; ++b) load2(a_s + b * p.a_box * 128, &tmA, k0, a0 + b * p.a_box);
+            if constexpr (!C::B_MN) {
+              load3(b_s, &tmB, k0, b0);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 128 / C::kChunk; ++c)
+                load3(b_s + c * C::BK * 128, &tmB, b0 + c * C::kChunk, k0);
+            }
+          }
+        }
+        if (tail) {
+          if (!__all_sync(0xffffffffu, mbar_wait(tail_bar, ntail & 1u))) {
+            if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 62);
+            ok = false;
+            break;
+          }
+          ++ntail;
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 4; ++c) {
+            uint8_t* chunk = smem + s * C::kStage + c * 8192;
+            for (int i = valid * 8 + int(lane); i < 512; i += 32) reinterpret_cast<uint4*>(chunk)[i] = z;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (C::PAIR) mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
+            else mbar_arrive(full_bar(s));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // Do not leave while copies may still be landing (after an error; else all are consumed).
+    if (!ok && it > 0 && rank == 0) {
+      for (uint32_t k = 0; k < uint32_t(C::STAGES) && k < it; ++k) {
+        const uint32_t i2 = it - 1 - k;
+        mbar_wait(full_bar(i2 % C::STAGES), (i2 / C::STAGES) & 1u, kDrainNs);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = C::F8 ? make_idesc_e4m3(C::BM, C::BN, C::A_MN, C::B_MN)
+                                       : make_idesc_bf16(C::BM, C::BN, C::A_MN, C::B_MN);
+      // K advance per instruction (32 bytes of K): inside a K-major row, or that many
+      // 128-byte rows of an MN-major tile.
+      constexpr uint32_t mn_adv = (32u / C::kElem) * 128u;
+      constexpr uint32_t a_adv = C::A_MN ? mn_adv : 32u, b_adv = C::B_MN ? mn_adv : 32u;
+      constexpr uint32_t mn_lbo = C::BK * 128u;   // bytes between MN-major column chunks
+      constexpr uint32_t a_lbo = C::A_MN ? mn_lbo : 16u, b_lbo = C::B_MN ? mn_lbo : 16u;
+      uint32_t it = 0, u = 0;
+      int e = 0;
+      bool ok = true;
+      for (int t = unit; t < num_tiles && ok; t += units) {
+        const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
+        for (int kb = 0; kb < x.nk; ++kb, ++it) {
+          const uint32_t buf = u & 1u;
+          if (C::F8 || kb == 0) {
+            if (!(C::PAIR ? mbar_wait_cluster(tempty_bar(buf), ((u >> 1) & 1u) ^ 1u)
+                          : mbar_wait(tempty_bar(buf), ((u >> 1) & 1u) ^ 1u))) {
+              set_status_site(p.status, QLORA_ERR_TIMEOUT, 63);
+              ok = false;
+              break;
+            }
+          }
+          const int s = it % C::STAGES;
+          const uint32_t ph = (it / C::STAGES) & 1u;
+          if (!(C::PAIR ? mbar_wait_cluster(full_bar(s), ph) : mbar_wait(full_bar(s), ph))) {
+            set_status_site(p.status, QLORA_ERR_TIMEOUT, 64);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = base + s * C::kStage;
+          const uint64_t ad = make_smem_desc(st, a_lbo, 1024u, kSwizzle128B);
+          const uint64_t bd = make_smem_desc(st + C::kA, b_lbo, 1024u, kSwizzle128B);
+          const uint32_t d = tmem + buf * C::BN;
+#pragma unroll
+          for (uint32_t kk = 0; kk < 4; ++kk) {
+            const uint64_t a2 = ad + uint64_t((kk * a_adv) >> 4), b2 = bd + uint64_t((kk * b_adv) >> 4);
+            const uint32_t acc = (kk > 0 || (!C::F8 && kb > 0)) ? 1u : 0u;
+            if constexpr (C::PAIR) {
+              if constexpr (C::F8) tc_mma_f8_pair(d, a2, b2, idesc, acc);
+              else tc_mma_bf16_pair(d, a2, b2, idesc, acc);
+            } else {
+              if constexpr (C::F8) tc_mma_f8(d, a2, b2, idesc, acc);
+              else tc_mma_bf16(d, a2, b2, idesc, acc);
+            }
+          }
+          if constexpr (C::PAIR) tc_commit_pair_mc(empty_bar(s), 3);
+          else tc_commit(empty_bar(s));
+          if (C::F8 || kb == x.nk - 1) {
+            if constexpr (C::PAIR) tc_commit_pair_mc(tfull_bar(buf), 3);
+            else tc_commit(tfull_bar(buf));
+            ++u;
+          }
+        }
+      }
+      // All MMAs of this thread are complete once drain_bar flips.
+      if constexpr (C::PAIR) tc_commit_pair_mc(drain_bar, 1);
+      else tc_commit(drain_bar);
+      mbar_wait(drain_bar, 0, kDrainNs);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const uint32_t q = warp & 3u;                 // TMEM lane quadrant this warp may read
+    const int cg = int(warp - 2) >> 2;            // 64-column group
+    const uint32_t stage_off = C::STAGES * C::kStage + (warp - 2) * 4096u;
+    const uint32_t stg = base + stage_off;
+    const uint32_t trow = tmem + ((q * 32u) << 16) + cg * 64;
+    uint32_t u = 0;
+    int e = 0;
+    bool ok = true;
+    for (int t = unit; t < num_tiles && ok; t += units) {
+      const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
+      const int first = int(rank) * 128 + int(q) * 32;       // this warp's first row in the tile
+      const int rows = min(32, x.rows - first);              // rows to store (may be <= 0)
+      const int col0 = x.n0 + cg * 64;
+      uint64_t acc[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[i] = 0;
+      const float* sa = nullptr;
+      const float* sb = nullptr;
+      float s_next = 0.f;
+      if constexpr (C::F8) {
+        sa = p.sa + int64_t(x.row0 + first + min(int(lane), max(rows, 1) - 1)) * p.nb_a;
+        sb = p.sb + x.e * p.sb_e + min(col0 >> 7, p.nb_n - 1) * p.sb_n;
+        if (rows > 0) s_next = __ldg(sa) * __ldg(sb);
+      }
+      const int reads = C::F8 ? x.nk : (x.nk > 0 ? 1 : 0);
+      for (int k = 0; k < reads; ++k, ++u) {
+        const uint32_t buf = u & 1u;
+        const float s = s_next;
+        if (C::F8 && k + 1 < reads && rows > 0) s_next = __ldg(sa + k + 1) * __ldg(sb + (k + 1) * p.sb_k);
+        if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), (u >> 1) & 1u))) {
+          if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 65);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t s2 = dup2(C::F8 ? s : 1.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(trow + buf * C::BN + h * 32, v);
+          tmem_ld_wait_for(v);
+          if (h == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (C::PAIR) mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
+              else mbar_arrive(tempty_bar(buf));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fma2(acc[h * 16 + i], v[2 * i], v[2 * i + 1], s2);
+        }
+      }
+      if (!ok) break;
+      if (rows <= 0 || col0 >= p.n_cols) continue;
+      // Through this warp's staging rows (128-byte swizzle) to global memory: by TMA, or row
+      // by row where the group ends inside the 32 rows.
+      constexpr int kPasses = C::DW ? 2 : 1;
+#pragma unroll
+      for (int ps = 0; ps < kPasses; ++ps) {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint4 o;
+          if constexpr (C::DW) {
+            unpack2(acc[ps * 16 + 2 * c], o.x, o.y);
+            unpack2(acc[ps * 16 + 2 * c + 1], o.z, o.w);
+          } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack2(acc[4 * c + i], w[2 * i], w[2 * i + 1]);
+            o.x = pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+            o.y = pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+            o.z = pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5]));
+            o.w = pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7]));
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128u + ((uint32_t(c) ^ (lane & 7u)) << 4)),
+                       "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
+                       : "memory");
+        }
+        const int row = x.row0 + first;
+        if (C::DW || rows == 32) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (C::DW) {
+              if (col0 + 32 * ps < p.n_cols) tma_store_3d(&tmD, stg, col0 + 32 * ps, row, x.e);
+            } else {
+              tma_store_2d(&tmD, stg, col0, row);
+            }
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + int(lane >> 3), c = int(lane & 7u);
+            uint32_t v[4];
+            lds_u4(stg + r * 128u + ((uint32_t(c) ^ (r & 7u)) << 4), v);
+            if (r < rows && col0 + c * 8 < p.n_cols)
+              *reinterpret_cast<uint4*>(p.d + int64_t(row + r) * p.ld_d + col0 + c * 8) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (C::PAIR) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (C::PAIR) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// --------------------------------------------------------------- host side
+
+constexpr int kMaxDevices = 64;
+
+// CTAs (single) or pairs that run at once on the current device; sets the kernel's
+// shared-memory limit on the device's first use. 0 on failure.
+template <class C>
+int resident_units() {
+  static std::atomic<int> cache[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = cache[dev].load(std::memory_order_acquire);
+  if (n > 0) return n;
+  if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+    return 0;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
+  n = sms;
+  if (C::PAIR) {
+    cudaLaunchConfig_t qc = {};
+    cudaLaunchAttribute qa[1];
+    qa[0].id = cudaLaunchAttributeClusterDimension;
+    qa[0].val.clusterDim.x = 2;
+    qa[0].val.clusterDim.y = 1;
+    qa[0].val.clusterDim.z = 1;
+    qc.gridDim = dim3(sms / 2 * 2, 1, 1);
+    qc.blockDim = dim3(C::kThreads, 1, 1);
+    qc.dynamicSmemBytes = C::kSmem;
+    qc.attrs = qa;
+    qc.numAttrs = 1;
+    n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, expert_gemm_kernel<C>, &qc) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sms / 2;
+    }
+  }
+  cache[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+template <class C>
+qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
+  const int max_units = resident_units<C>();
+  if (max_units <= 0) return QLORA_ERR_CUDA;
+  const TmapType ty = C::F8 ? TmapType::U8 : TmapType::BF16;
+  const bool dw = C::DW, fwd = a.mode == ExpertMode::Fwd;
+  const int64_t K = fwd ? a.in : a.out;         // Fwd, Dx: reduction length
+  const int64_t N = fwd ? a.out : a.in;         // columns of D
+  ExpertParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = int(a.M);
+  p.E = int(a.E);
+  p.n_cols = int(N);
+  p.tiles_n = int((N + C::BN - 1) / C::BN);
+  p.tiles_r = int((a.out + C::BM - 1) / C::BM);
+  p.nk = int((K + C::BK - 1) / C::BK);
+  p.d_rows = int(a.out);
+  // Groups of a few rows: boxes of 32 rows, so that a tile's unused rows are not fetched.
+  p.a_box = (!C::PAIR && a.M < 64 * a.E) ? 32 : 128;
+  p.offsets = a.offsets;
+  p.sa = a.sa;
+  p.sb = a.sb;
+  p.nb_a = int((K + 127) / 128);
+  p.nb_n = int((N + 127) / 128);
+  const int64_t nbo = (a.out + 127) / 128, nbi = (a.in + 127) / 128;
+  p.sb_e = nbo * nbi;
+  p.sb_n = fwd ? nbi : 1;
+  p.sb_k = fwd ? 1 : nbi;
+  p.d = static_cast<uint16_t*>(a.d);
+  p.ld_d = N;
+  p.status = a.status;
+
+  CUtensorMap A, B, D;
+  bool good;
+  if (dw) {
+    good = make_tmap_2d(&A, a.a, ty, a.out, a.M, a.out * C::kElem, 64, 64, true) &&
+           make_tmap_2d(&B, a.b, ty, a.in, a.M, a.in * C::kElem, 64, 64, true) &&
+           make_tmap_3d(&D, a.d, TmapType::F32, a.in, a.out, a.E, 32, 32);
+  } else {
+    good = make_tmap_2d(&A, a.a, ty, K, a.M, K * C::kElem, C::BK, p.a_box, true) &&
+           make_tmap_3d(&B, a.b, ty, a.in, a.out, a.E, 128 / C::kElem, C::B_MN ? C::BK : 128) &&
+           make_tmap_2d(&D, a.d, TmapType::BF16, N, a.M, N * 2, 64, 32, true);
+  }
+  if (!good) return QLORA_ERR_CUDA;
+
+  // Row tiles at most: every group may end inside a tile.
+  const int64_t row_tiles = dw ? a.E * p.tiles_r
+                               : std::min<int64_t>(a.M, (a.M + C::BM - 1) / C::BM + (a.offsets ? a.E - 1 : 0));
+  const int64_t num_tiles = row_tiles * p.tiles_n;
+  if (num_tiles > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;
+  const int units = int(std::min<int64_t>(num_tiles, max_units));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(units * (C::PAIR ? 2 : 1)), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  const int skip = pdl_enabled() ? 0 : 1;
+  cfg.attrs = attr + skip;
+  cfg.numAttrs = (C::PAIR ? 2 : 1) - skip;
+  if (cudaLaunchKernelEx(&cfg, expert_gemm_kernel<C>, A, B, D, p) != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return QLORA_OK;
+}
+
+template <bool F8, ExpertMode MODE>
+qlora_status launch_mode(const ExpertArgs& a, cudaStream_t s) {
+  // Pair tiles halve the L2 bytes per product; single tiles waste fewer rows of small groups.
+  const int64_t N = MODE == ExpertMode::Fwd ? a.out : a.in;
+  const int64_t rows = MODE == ExpertMode::Dw ? a.out : a.M / a.E;
+  const bool pair = rows >= 192 && N >= 256;
+  if (pair) return launch_cfg<ExpertCfg<true, F8, MODE>>(a, s);
+  return launch_cfg<ExpertCfg<false, F8, MODE>>(a, s);
+}
+
+}  // namespace
+
+qlora_status launch_expert_gemm(const ExpertArgs& a, cudaStream_t s) {
+  switch (a.mode) {
+    case ExpertMode::Fwd:
+      return a.f8 ? launch_mode<true, ExpertMode::Fwd>(a, s) : launch_mode<false, ExpertMode::Fwd>(a, s);
+    case ExpertMode::Dx:
+      return a.f8 ? launch_mode<true, ExpertMode::Dx>(a, s) : launch_mode<false, ExpertMode::Dx>(a, s);
+    case ExpertMode::Dw:
+      return a.f8 ? QLORA_ERR_UNSUPPORTED : launch_mode<false, ExpertMode::Dw>(a, s);
+  }
+  return QLORA_ERR_UNSUPPORTED;
+}
+
+}  // namespace qlb

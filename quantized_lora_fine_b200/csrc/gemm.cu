@@ -1299,6 +1299,23 @@ bool make_tmap_2d_sw(CUtensorMap* m, const void* base, TmapType type, uint64_t i
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_3d(CUtensorMap* m, const void* base, TmapType type, uint64_t inner, uint64_t rows, uint64_t depth,
+                  uint32_t box_inner, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  uint64_t elem = 2;
+  if (type == TmapType::U8) { dt = CU_TENSOR_MAP_DATA_TYPE_UINT8; elem = 1; }
+  if (type == TmapType::F32) { dt = CU_TENSOR_MAP_DATA_TYPE_FLOAT32; elem = 4; }
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {inner * elem, inner * rows * elem};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int num_sms() {
   static int n = 0;
   if (n == 0) {

@@ -89,6 +89,10 @@ bool make_tmap_2d(CUtensorMap* m, const void* base, TmapType type, uint64_t inne
 // Same with an explicit swizzle: 0 none, 32, 64 or 128 (bytes).
 bool make_tmap_2d_sw(CUtensorMap* m, const void* base, TmapType type, uint64_t inner, uint64_t outer,
                      uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes);
+// 3-D tensor map of `depth` dense row-major [rows x inner] matrices: box of
+// box_inner x box_rows elements of one matrix, 128-byte swizzle.
+bool make_tmap_3d(CUtensorMap* m, const void* base, TmapType type, uint64_t inner, uint64_t rows, uint64_t depth,
+                  uint32_t box_inner, uint32_t box_rows);
 
 qlora_status launch_gemm(GemmKind kind, int bn, const GemmOperands& o, const GemmParams& p, cudaStream_t s);
 

@@ -506,8 +506,11 @@ typedef struct {
 size_t qlora_expert_workspace_size(void);
 
 /* Linear with an e4m3 weight (experts = 1) and e4m3 rows, products summed in fp32:
- * Y [M x out] = X W^T, and for the backward of the frozen weight dX [M x in] = dY W. */
-qlora_status fp8_linear_fwd(const qlora_expert_weight* w, const uint8_t* x_codes, const float* x_scale, int64_t M,
+ * Y [M x out] = X W^T, and for the backward of the frozen weight dX [M x in] = dY W.
+ * X: e4m3 codes with x_scale, or, for up to fp8_linear_bf16_rows() rows, bf16 values
+ * with x_scale NULL, which are quantized as fp8_quantize_rows does within the call. */
+int64_t fp8_linear_bf16_rows(void);
+qlora_status fp8_linear_fwd(const qlora_expert_weight* w, const void* X, const float* x_scale, int64_t M,
                             uint16_t* Y, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
 qlora_status fp8_linear_bwd(const qlora_expert_weight* w, const uint8_t* dy_codes, const float* dy_scale, int64_t M,
                             uint16_t* dX, void* workspace, size_t workspace_bytes, qlora_stream_t stream);

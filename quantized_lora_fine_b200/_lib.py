@@ -91,6 +91,7 @@ SIGNATURES = {
     "fp8_quantize_weight": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                     c_size_t, c_void_p]),
     "qlora_expert_workspace_size": (c_size_t, []),
+    "fp8_linear_bf16_rows": (c_int64, []),
     "fp8_linear_fwd": (c_int, [POINTER(ExpertWeight), c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_size_t,
                                c_void_p]),
     "fp8_linear_bwd": (c_int, [POINTER(ExpertWeight), c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_size_t,

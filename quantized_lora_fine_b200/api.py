@@ -424,52 +424,35 @@ def rank_errors(err: torch.Tensor, K: int):
 
 # ------------------------------------------------------------------ norm, 8-bit and grouped linears
 
-_F8 = torch.float8_e4m3fn
+_F8, _BF16, _F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _blocks(n: int) -> int:
-    return (n + 127) // 128
+    return (n + 127) >> 7
 
 
-class _On:
-    """Makes `device` current for a call and gives its current stream; every tensor of the
-    call must be there."""
-    __slots__ = ("index", "prev")
-
-    def __init__(self, device: torch.device, *tensors: Optional[torch.Tensor]):
-        for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError(f"every tensor of a call must be on one device: got {device} and {t.device}")
-        self.index = device.index
-
-    def __enter__(self) -> int:
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.index:
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.prev != self.index:
-            torch.cuda.set_device(self.prev)
+def _check(t: torch.Tensor, dtype, shape: Optional[tuple], name: str, device: Optional[int] = None):
+    """t is a contiguous CUDA tensor of this dtype, shape (None: any 2-D one) and device."""
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous() and
+            (t.dim() == 2 if shape is None else t.shape == shape)):
+        _need(t, dtype, name)
+        raise ValueError(f"{name} must be 2-D" if shape is None else
+                         f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"every tensor of a call must be on one device: {name} is on cuda:{t.get_device()}, "
+                         f"not cuda:{device}")
 
 
-def _need_shape(t: torch.Tensor, shape: Tuple[int, ...], name: str):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _need_rows(t: torch.Tensor, name: str):
-    _need(t, torch.bfloat16, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
-
-
-def _out(t: Optional[torch.Tensor], shape: Tuple[int, ...], dtype, device, name: str) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, name)
-    _need_shape(t, shape, name)
-    return t
+def _check_weight_vector(w: torch.Tensor, H: int, device: int) -> int:
+    if w.dtype is _BF16:
+        _check(w, _BF16, (H,), "weight", device)
+        return DTYPE_BF16
+    if w.dtype is not _F32:
+        raise ValueError("weight must be bf16 or fp32")
+    _check(w, _F32, (H,), "weight", device)
+    return DTYPE_F32
 
 
 @dataclasses.dataclass
@@ -480,11 +463,9 @@ class FP8Rows:
     scale: torch.Tensor
 
     def __post_init__(self):
-        _need(self.codes, _F8, "codes")
-        _need(self.scale, torch.float32, "scale")
-        if self.codes.dim() != 2:
-            raise ValueError("codes must be 2-D")
-        _need_shape(self.scale, (self.codes.shape[0], _blocks(self.codes.shape[1])), "scale")
+        _check(self.codes, _F8, None, "codes")
+        M, n = self.codes.shape
+        _check(self.scale, _F32, (M, _blocks(n)), "scale", self.codes.get_device())
 
 
 @dataclasses.dataclass
@@ -496,12 +477,12 @@ class FP8Weight:
     scale: torch.Tensor
 
     def __post_init__(self):
-        _need(self.codes, _F8, "codes")
-        _need(self.scale, torch.float32, "scale")
-        if self.codes.dim() not in (2, 3):
+        shape = self.codes.shape
+        if len(shape) not in (2, 3):
             raise ValueError("codes must be [out, in] or [experts, out, in]")
-        o, i = self.codes.shape[-2:]
-        _need_shape(self.scale, tuple(self.codes.shape[:-2]) + (_blocks(o), _blocks(i)), "scale")
+        _check(self.codes, _F8, shape, "codes")
+        _check(self.scale, _F32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), "scale",
+               self.codes.get_device())
 
     @property
     def out(self) -> int:
@@ -512,21 +493,26 @@ class FP8Weight:
         return self.codes.shape[-1]
 
 
-def _expert_weight(W) -> Tuple[_lib.ExpertWeight, int, int, int]:
+def _new_rows(M: int, n: int, device) -> FP8Rows:
+    r = object.__new__(FP8Rows)
+    r.codes = torch.empty((M, n), dtype=_F8, device=device)
+    r.scale = torch.empty((M, _blocks(n)), dtype=_F32, device=device)
+    return r
+
+
+def _expert_weight(W, device: int) -> Tuple[_lib.ExpertWeight, int, int, int]:
     """(descriptor, experts, out, in) of an FP8Weight or a bf16 tensor [(experts,) out, in]."""
-    s = _lib.ExpertWeight()
-    if isinstance(W, FP8Weight):
-        t = W.codes
-        s.codes, s.scale = t.data_ptr(), W.scale.data_ptr()
-    else:
-        t = W
-        _need(t, torch.bfloat16, "W")
-        if t.dim() not in (2, 3):
-            raise ValueError("W must be [out, in] or [experts, out, in]")
-        s.is_bf16, s.w_bf16 = 1, t.data_ptr()
-    s.experts = t.shape[0] if t.dim() == 3 else 1
-    s.out, s.in_ = t.shape[-2], t.shape[-1]
-    return s, s.experts, s.out, s.in_
+    t = W.codes if isinstance(W, FP8Weight) else W
+    shape = t.shape
+    E = shape[0] if len(shape) == 3 else 1
+    if t is not W:
+        _check(t, _F8, shape, "W.codes", device)
+        _check(W.scale, _F32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), "W.scale", device)
+        return _lib.ExpertWeight(E, shape[-2], shape[-1], 0, t.data_ptr(), W.scale.data_ptr(), None), E, *shape[-2:]
+    if len(shape) not in (2, 3):
+        raise ValueError("W must be [out, in] or [experts, out, in]")
+    _check(t, _BF16, shape, "W", device)
+    return _lib.ExpertWeight(E, shape[-2], shape[-1], 1, None, None, t.data_ptr()), E, *shape[-2:]
 
 
 def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -534,31 +520,29 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, resid
     """(y, h, rstd): h = bf16(x + residual) (x itself without a residual), rstd = 1 /
     sqrt(mean(h^2) + eps) per row, y = h rstd weight. y is bf16, or FP8Rows with fp8=True
     (quantized from the fp32 value). x: bf16 [M, H] with H % 8 == 0; weight: bf16 or fp32 [H]."""
-    _need_rows(x, "x")
+    _check(x, _BF16, None, "x")
+    dev = x.get_device()
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return rms_norm_fwd(x, weight, eps, residual, fp8)
     M, H = x.shape
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("weight must be bf16 or fp32")
-    _need(weight, weight.dtype, "weight")
-    _need_shape(weight, (H,), "weight")
-    if residual is not None:
-        _need(residual, torch.bfloat16, "residual")
-        _need_shape(residual, (M, H), "residual")
-    dev = x.device
-    lib = _lib.load()
-    with _On(dev, weight, residual) as stream:
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
-        h = x if residual is None else torch.empty_like(x)
-        if fp8:
-            q = FP8Rows(torch.empty((M, H), dtype=_F8, device=dev),
-                        torch.empty((M, _blocks(H)), dtype=torch.float32, device=dev))
-            y, y8, ys = None, q.codes.data_ptr(), q.scale.data_ptr()
-        else:
-            y, y8, ys = torch.empty_like(x), None, None
-        check(lib.qlora_rms_norm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(),
-                                     DTYPE_BF16 if weight.dtype == torch.bfloat16 else DTYPE_F32, M, H, float(eps),
-                                     None if residual is None else h.data_ptr(), _ptr(y), y8, ys, rstd.data_ptr(),
-                                     stream), "qlora_rms_norm_fwd")
-    return (q if fp8 else y), h, rstd
+    wt = _check_weight_vector(weight, H, dev)
+    if residual is None:
+        h, rp, hp = x, None, None
+    else:
+        _check(residual, _BF16, x.shape, "residual", dev)
+        h = torch.empty_like(x)
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    rstd = torch.empty(M, dtype=_F32, device=x.device)
+    if fp8:
+        y = _new_rows(M, H, x.device)
+        yp, qp, sp = None, y.codes.data_ptr(), y.scale.data_ptr()
+    else:
+        y = torch.empty_like(x)
+        yp, qp, sp = y.data_ptr(), None, None
+    check(_lib.load().qlora_rms_norm_fwd(x.data_ptr(), rp, weight.data_ptr(), wt, M, H, eps, hp, yp, qp, sp,
+                                         rstd.data_ptr(), _raw_stream(dev)), "qlora_rms_norm_fwd")
+    return y, h, rstd
 
 
 def rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
@@ -566,111 +550,134 @@ def rms_norm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: 
     """(dx, dw) from the gradient of y and, with dh, the one that reaches h itself: dx (bf16) is
     the gradient of x and of the residual alike, dw (fp32 [H]; None with need_dw=False) the
     weight's. h and rstd are rms_norm_fwd's. An 8-bit y counts as not rounded."""
-    _need_rows(dy, "dy")
+    _check(dy, _BF16, None, "dy")
+    dev = dy.get_device()
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return rms_norm_bwd(dy, h, rstd, weight, dh, need_dw)
     M, H = dy.shape
-    for t, nm in ((h, "h"), (dh, "dh")):
-        if t is not None:
-            _need(t, torch.bfloat16, nm)
-            _need_shape(t, (M, H), nm)
-    _need(rstd, torch.float32, "rstd")
-    _need_shape(rstd, (M,), "rstd")
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("weight must be bf16 or fp32")
-    _need(weight, weight.dtype, "weight")
-    _need_shape(weight, (H,), "weight")
-    dev = dy.device
+    _check(h, _BF16, dy.shape, "h", dev)
+    if dh is not None:
+        _check(dh, _BF16, dy.shape, "dh", dev)
+    _check(rstd, _F32, (M,), "rstd", dev)
+    wt = _check_weight_vector(weight, H, dev)
     lib = _lib.load()
-    with _On(dev, h, rstd, weight, dh) as stream:
-        dx = torch.empty_like(dy)
-        dw = torch.empty(H, dtype=torch.float32, device=dev) if need_dw else None
-        nbytes = lib.qlora_rms_norm_bwd_workspace_size(M, H) if need_dw else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None   # this call's alone
-        check(lib.qlora_rms_norm_bwd(dy.data_ptr(), _ptr(dh), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(),
-                                     DTYPE_BF16 if weight.dtype == torch.bfloat16 else DTYPE_F32, M, H,
-                                     dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, stream), "qlora_rms_norm_bwd")
+    dx = torch.empty_like(dy)
+    dw, ws, nbytes = None, None, 0
+    if need_dw:
+        dw = torch.empty(H, dtype=_F32, device=dy.device)
+        nbytes = lib.qlora_rms_norm_bwd_workspace_size(M, H)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)   # this call's alone
+    check(lib.qlora_rms_norm_bwd(dy.data_ptr(), _ptr(dh), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), wt, M, H,
+                                 dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, _raw_stream(dev)), "qlora_rms_norm_bwd")
     return dx, dw
 
 
 def fp8_quantize_rows(X: torch.Tensor) -> FP8Rows:
     """e4m3 codes of bf16 rows [M, in] with a scale for each 128 values (in % 16 == 0)."""
-    _need_rows(X, "X")
+    _check(X, _BF16, None, "X")
+    dev = X.get_device()
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return fp8_quantize_rows(X)
     M, inp = X.shape
-    lib = _lib.load()
-    with _On(X.device) as stream:
-        q = FP8Rows(torch.empty((M, inp), dtype=_F8, device=X.device),
-                    torch.empty((M, _blocks(inp)), dtype=torch.float32, device=X.device))
-        check(lib.fp8_quantize_rows(X.data_ptr(), M, inp, q.codes.data_ptr(), q.scale.data_ptr(), stream),
-              "fp8_quantize_rows")
+    q = _new_rows(M, inp, X.device)
+    check(_lib.load().fp8_quantize_rows(X.data_ptr(), M, inp, q.codes.data_ptr(), q.scale.data_ptr(),
+                                        _raw_stream(dev)), "fp8_quantize_rows")
     return q
 
 
 def fp8_quantize_weight(W: torch.Tensor) -> FP8Weight:
     """e4m3 codes of a bf16 or fp32 weight [out, in] or [experts, out, in] with a scale for each
     128 x 128 block. A non-finite weight is reported by status()."""
-    if W.dtype not in (torch.bfloat16, torch.float32):
+    if W.dtype not in (_BF16, _F32):
         raise ValueError("W must be bf16 or fp32")
     _need(W, W.dtype, "W")
     if W.dim() not in (2, 3):
         raise ValueError("W must be [out, in] or [experts, out, in]")
+    dev = W.get_device()
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return fp8_quantize_weight(W)
     o, i = W.shape[-2:]
-    lib = _lib.load()
-    with _On(W.device) as stream:
-        ws = Workspace.status_word(W.device.index)
-        w = FP8Weight(torch.empty(W.shape, dtype=_F8, device=W.device),
-                      torch.empty(tuple(W.shape[:-2]) + (_blocks(o), _blocks(i)), dtype=torch.float32,
-                                  device=W.device))
-        check(lib.fp8_quantize_weight(W.data_ptr(), DTYPE_BF16 if W.dtype == torch.bfloat16 else DTYPE_F32,
-                                      W.shape[0] if W.dim() == 3 else 1, o, i, w.codes.data_ptr(), w.scale.data_ptr(),
-                                      ws.data_ptr(), ws.numel(), stream), "fp8_quantize_weight")
-    return w
+    ws = Workspace.status_word(dev)
+    codes = torch.empty(W.shape, dtype=_F8, device=W.device)
+    scale = torch.empty((*W.shape[:-2], _blocks(o), _blocks(i)), dtype=_F32, device=W.device)
+    check(_lib.load().fp8_quantize_weight(W.data_ptr(), DTYPE_BF16 if W.dtype is _BF16 else DTYPE_F32,
+                                          W.shape[0] if W.dim() == 3 else 1, o, i, codes.data_ptr(), scale.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), _raw_stream(dev)), "fp8_quantize_weight")
+    return FP8Weight(codes, scale)
 
 
-def _fp8_linear(fn: str, w: FP8Weight, rows, cols_in: int, cols_out: int, out: Optional[torch.Tensor], name: str):
-    if not isinstance(w, FP8Weight) or w.codes.dim() != 2:
-        raise ValueError("w must be an FP8Weight [out, in]")
-    if not isinstance(rows, FP8Rows):
-        rows = fp8_quantize_rows(rows)
-    M = rows.codes.shape[0]
-    _need_shape(rows.codes, (M, cols_in), name)
-    dev = rows.codes.device
-    cs = _expert_weight(w)[0]
-    lib = _lib.load()
-    with _On(dev, rows.scale, w.codes, w.scale, out) as stream:
-        ws = Workspace.status_word(dev.index)
-        out = _out(out, (M, cols_out), torch.bfloat16, dev, "out")
-        check(getattr(lib, fn)(ctypes.byref(cs), rows.codes.data_ptr(), rows.scale.data_ptr(), M, out.data_ptr(),
-                               ws.data_ptr(), ws.numel(), stream), fn)
-    return out
+def _rows_of(rows, eight_bit: bool, cols: int, name: str):
+    """(tensor, scale or None, device) of a product's rows: FP8Rows, or bf16, which is quantized
+    where the weight is 8 bit."""
+    if isinstance(rows, FP8Rows):
+        if not eight_bit:
+            raise ValueError(f"{name}: FP8Rows need an FP8Weight")
+        t, sc = rows.codes, rows.scale
+        dev = t.get_device()
+        _check(t, _F8, None, name)
+        _check(sc, _F32, (t.shape[0], _blocks(t.shape[1])), name + ".scale", dev)
+    else:
+        _check(rows, _BF16, None, name)
+        t, sc, dev = rows, None, rows.get_device()
+    if t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns, got {t.shape[1]}")
+    return t, sc, dev
+
+
+def _output(t: Optional[torch.Tensor], shape: tuple, dtype, like: torch.Tensor, dev: int, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _check(t, dtype, shape, name, dev)
+    return t
 
 
 def fp8_linear_fwd(w: FP8Weight, X, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = X W^T (bf16 [M, out]) with e4m3 weight and rows. X: FP8Rows, or bf16 [M, in], which is
     quantized first."""
-    return _fp8_linear("fp8_linear_fwd", w, X, w.inp, w.out, Y, "X")
+    if not isinstance(w, FP8Weight) or w.codes.dim() != 2:
+        raise ValueError("w must be an FP8Weight [out, in]")
+    x, sx, dev = _rows_of(X, True, w.inp, "X")
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return fp8_linear_fwd(w, X, Y)
+    cs = _expert_weight(w, dev)[0]
+    lib = _lib.load()
+    M = x.shape[0]
+    if sx is None and M > _FP8_BF16_ROWS:
+        q = fp8_quantize_rows(x)
+        x, sx = q.codes, q.scale
+    ws = Workspace.status_word(dev)
+    Y = _output(Y, (M, w.out), _BF16, x, dev, "Y")
+    check(lib.fp8_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), M, Y.data_ptr(), ws.data_ptr(), 256,
+                             _raw_stream(dev)), "fp8_linear_fwd")
+    return Y
+
+
+# Rows up to which fp8_linear_fwd takes bf16 and quantizes within its kernel (fp8_linear_bf16_rows()).
+_FP8_BF16_ROWS = 8
 
 
 def fp8_linear_bwd(w: FP8Weight, dY, dX: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX = dY W (bf16 [M, in]), the gradient through the frozen weight. dY: FP8Rows, or bf16
     [M, out], which is quantized first."""
-    return _fp8_linear("fp8_linear_bwd", w, dY, w.out, w.inp, dX, "dY")
-
-
-def _grouped_rows(W, rows, cols: int, name: str):
-    """(tensor, scale or None) of a grouped call's rows in the weight's kind."""
-    if isinstance(W, FP8Weight):
-        if not isinstance(rows, FP8Rows):
-            rows = fp8_quantize_rows(rows)
-        t, sc = rows.codes, rows.scale
-    else:
-        _need_rows(rows, name)
-        t, sc = rows, None
-    _need_shape(t, (t.shape[0], cols), name)
-    return t, sc
-
-
-def _need_offsets(offsets: torch.Tensor, E: int):
-    _need(offsets, torch.int32, "offsets")
-    _need_shape(offsets, (E + 1,), "offsets")
+    if not isinstance(w, FP8Weight) or w.codes.dim() != 2:
+        raise ValueError("w must be an FP8Weight [out, in]")
+    d, sd, dev = _rows_of(dY, True, w.out, "dY")
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return fp8_linear_bwd(w, dY, dX)
+    cs = _expert_weight(w, dev)[0]
+    if sd is None:
+        q = fp8_quantize_rows(d)
+        d, sd = q.codes, q.scale
+    ws = Workspace.status_word(dev)
+    dX = _output(dX, (d.shape[0], w.inp), _BF16, d, dev, "dX")
+    check(_lib.load().fp8_linear_bwd(ctypes.byref(cs), d.data_ptr(), sd.data_ptr(), d.shape[0], dX.data_ptr(),
+                                     ws.data_ptr(), 256, _raw_stream(dev)), "fp8_linear_bwd")
+    return dX
 
 
 def grouped_linear_fwd(W, X, offsets: torch.Tensor, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -678,17 +685,21 @@ def grouped_linear_fwd(W, X, offsets: torch.Tensor, Y: Optional[torch.Tensor] = 
     W: bf16 [experts, out, in] with bf16 X [M, in], or an FP8Weight with FP8Rows (bf16 X is
     quantized first). offsets: int32 [experts + 1] on the device, ascending within 0 .. M; rows
     outside every group are not written (pass Y to keep what is in them)."""
-    cs, E, o, i = _expert_weight(W)
-    _need_offsets(offsets, E)
-    x, sx = _grouped_rows(W, X, i, "X")
-    M, dev = x.shape[0], x.device
-    lib = _lib.load()
-    with _On(dev, sx, W.codes if sx is not None else W, offsets, Y) as stream:
-        ws = Workspace.status_word(dev.index)
-        Y = _out(Y, (M, o), torch.bfloat16, dev, "Y")
-        check(lib.qlora_grouped_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), M, offsets.data_ptr(),
-                                           Y.data_ptr(), ws.data_ptr(), ws.numel(), stream),
-              "qlora_grouped_linear_fwd")
+    eight = isinstance(W, FP8Weight)
+    x, sx, dev = _rows_of(X, eight, W.inp if eight else W.shape[-1], "X")
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return grouped_linear_fwd(W, X, offsets, Y)
+    cs, E, o, _ = _expert_weight(W, dev)
+    _check(offsets, torch.int32, (E + 1,), "offsets", dev)
+    if eight and sx is None:
+        q = fp8_quantize_rows(x)
+        x, sx = q.codes, q.scale
+    ws = Workspace.status_word(dev)
+    Y = _output(Y, (x.shape[0], o), _BF16, x, dev, "Y")
+    check(_lib.load().qlora_grouped_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), x.shape[0],
+                                               offsets.data_ptr(), Y.data_ptr(), ws.data_ptr(), 256,
+                                               _raw_stream(dev)), "qlora_grouped_linear_fwd")
     return Y
 
 
@@ -697,27 +708,33 @@ def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, 
     """(dX, dW) of grouped_linear_fwd: dX_e = dY_e W_e (bf16 [M, in]; rows outside every group are
     not written) and dW_e = dY_e^T X_e (fp32 [experts, out, in], zero for an expert without rows;
     bf16 weights only: an FP8Weight is frozen, pass need_dW=False). X may be None without dW."""
-    cs, E, o, i = _expert_weight(W)
-    _need_offsets(offsets, E)
+    eight = isinstance(W, FP8Weight)
     if not need_dX and not need_dW:
         raise ValueError("need_dX or need_dW must be true")
-    if need_dW and isinstance(W, FP8Weight):
+    if need_dW and eight:
         raise ValueError("an FP8Weight is frozen: pass need_dW=False")
-    dy, sy = _grouped_rows(W, dY, o, "dY")
-    M, dev = dy.shape[0], dy.device
+    d, sd, dev = _rows_of(dY, eight, W.out if eight else W.shape[-2], "dY")
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return grouped_linear_bwd(W, X, dY, offsets, need_dX, need_dW, dX, dW)
+    cs, E, o, i = _expert_weight(W, dev)
+    _check(offsets, torch.int32, (E + 1,), "offsets", dev)
+    M = d.shape[0]
+    xp = None
     if need_dW:
         if X is None:
             raise ValueError("X is needed for dW")
-        _need_rows(X, "X")
-        _need_shape(X, (M, i), "X")
-    lib = _lib.load()
-    with _On(dev, sy, W.codes if sy is not None else W, offsets, X if need_dW else None, dX, dW) as stream:
-        ws = Workspace.status_word(dev.index)
-        dX = _out(dX, (M, i), torch.bfloat16, dev, "dX") if need_dX else None
-        dW = _out(dW, (E, o, i), torch.float32, dev, "dW") if need_dW else None
-        check(lib.qlora_grouped_linear_bwd(ctypes.byref(cs), _ptr(X) if need_dW else None, dy.data_ptr(), _ptr(sy), M,
-                                           offsets.data_ptr(), _ptr(dX), _ptr(dW), ws.data_ptr(), ws.numel(), stream),
-              "qlora_grouped_linear_bwd")
+        _check(X, _BF16, (M, i), "X", dev)
+        xp = X.data_ptr()
+    if eight and sd is None:
+        q = fp8_quantize_rows(d)
+        d, sd = q.codes, q.scale
+    ws = Workspace.status_word(dev)
+    dX = _output(dX, (M, i), _BF16, d, dev, "dX") if need_dX else None
+    dW = _output(dW, (E, o, i), _F32, d, dev, "dW") if need_dW else None
+    check(_lib.load().qlora_grouped_linear_bwd(ctypes.byref(cs), xp, d.data_ptr(), _ptr(sd), M, offsets.data_ptr(),
+                                               _ptr(dX), _ptr(dW), ws.data_ptr(), 256, _raw_stream(dev)),
+          "qlora_grouped_linear_bwd")
     return dX, dW
 
 

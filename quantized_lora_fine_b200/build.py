@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora_b200.so")
-SOURCES = ["codec.cu", "layer_error.cu", "gemm.cu", "block8.cu", "norm.cu", "expert_gemm.cu", "capi.cu", "capi_blocks.cu"]
+SOURCES = ["codec.cu", "layer_error.cu", "gemm.cu", "block8.cu", "norm.cu", "expert_gemm.cu", "few_rows.cu", "capi.cu", "capi_blocks.cu"]
 HEADERS = ["internal.cuh", "nf4_device.cuh", "nf4_constants.cuh", "ptx.cuh", "gemm.cuh", "block8.cuh",
            "expert_gemm.cuh"]
 

@@ -52,12 +52,13 @@ qlora_status check_status_ws(const void* ws, size_t bytes) {
 }
 
 // One product of rows `a` (bf16, or codes with scales `sa`) with the experts' weights.
-qlora_status check_rows(const qlora_expert_weight* w, const void* a, const float* sa, int64_t M) {
+qlora_status check_rows(const qlora_expert_weight* w, const void* a, const float* sa, int64_t M,
+                        bool may_be_bf16 = false) {
   if (M <= 0 || M > kMaxRows) return QLORA_ERR_SHAPE;
   if (!a) return QLORA_ERR_NULL;
   if (!aligned16(a)) return QLORA_ERR_ALIGN;
   if (!w->is_bf16) {
-    if (!sa) return QLORA_ERR_NULL;
+    if (!sa && !(may_be_bf16 && M <= kFewQuantRows)) return QLORA_ERR_NULL;
     if (!aligned4(sa)) return QLORA_ERR_ALIGN;
   }
   return QLORA_OK;
@@ -79,6 +80,7 @@ qlora_status product(ExpertMode mode, const qlora_expert_weight* w, const void* 
   e.sb = w->scale;
   e.d = d;
   e.status = static_cast<int*>(ws);
+  if (e.f8 && !sa) return launch_few_rows(e, true, S(stream));
   return launch_expert_gemm(e, S(stream));
 }
 
@@ -146,22 +148,24 @@ qlora_status fp8_quantize_weight(const void* W, int32_t w_dtype, int64_t experts
 
 size_t qlora_expert_workspace_size(void) { return kStatusBytes; }
 
-static qlora_status fp8_linear(bool fwd, const qlora_expert_weight* w, const uint8_t* codes, const float* scale,
+int64_t fp8_linear_bf16_rows(void) { return kFewQuantRows; }
+
+static qlora_status fp8_linear(bool fwd, const qlora_expert_weight* w, const void* rows, const float* scale,
                                int64_t M, uint16_t* d, void* ws, size_t ws_bytes, qlora_stream_t stream) {
   QLB_TRY(check_expert_weight(w));
   if (w->is_bf16) return QLORA_ERR_UNSUPPORTED;
   if (w->experts != 1) return QLORA_ERR_SHAPE;
-  QLB_TRY(check_rows(w, codes, scale, M));
+  QLB_TRY(check_rows(w, rows, scale, M, fwd));
   if (!d) return QLORA_ERR_NULL;
   if (!aligned16(d)) return QLORA_ERR_ALIGN;
   QLB_TRY(check_status_ws(ws, ws_bytes));
   QLB_TRY(device_ok());
-  return product(fwd ? ExpertMode::Fwd : ExpertMode::Dx, w, codes, scale, M, nullptr, d, ws, stream);
+  return product(fwd ? ExpertMode::Fwd : ExpertMode::Dx, w, rows, scale, M, nullptr, d, ws, stream);
 }
 
-qlora_status fp8_linear_fwd(const qlora_expert_weight* w, const uint8_t* x_codes, const float* x_scale, int64_t M,
+qlora_status fp8_linear_fwd(const qlora_expert_weight* w, const void* X, const float* x_scale, int64_t M,
                             uint16_t* Y, void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
-  return fp8_linear(true, w, x_codes, x_scale, M, Y, workspace, workspace_bytes, stream);
+  return fp8_linear(true, w, X, x_scale, M, Y, workspace, workspace_bytes, stream);
 }
 
 qlora_status fp8_linear_bwd(const qlora_expert_weight* w, const uint8_t* dy_codes, const float* dy_scale, int64_t M,

@@ -19,8 +19,12 @@
 // feeds twice the products that it does in a 128 x 128 tile). Roles:
 //   warp 0      TMA producer
 //   warp 1      TMEM allocation, MMA issue (even CTA of a pair)
-//   warps 2..   epilogue, 4 lane quadrants x (tile columns / 64): each warp owns 32
-//               rows x 64 columns, in registers
+//   warps 2, 3  (e4m3 only) scales of A's rows to shared memory, four steps at a time
+//   warps 4..   epilogue, 4 lane quadrants x column groups: each warp owns 32 rows x 128
+//               columns (64 in single tiles), in registers
+// In a pair a thread holds 128 sums and 32 values in flight; the first warpgroup gives up
+// registers for that (168 x 384 = 88 x 128 + 208 x 256). 16 epilogue warps of 64 columns
+// have 96 registers at most and spill.
 // Stage: 128 rows (or columns) x 128 bytes of K for each operand, 128-byte swizzle,
 // K-major as stored along K, MN-major where the reduction runs over rows.
 //
@@ -63,6 +67,7 @@ struct ExpertParams {
   const float* sa;
   const float* sb;
   int nb_a;              // scales per row of A
+  int sa_vec;            // rows of scales start on 16 bytes
   int nb_n;              // column blocks of sb (clamps the ragged last tile)
   int64_t sb_e, sb_n, sb_k;   // strides of sb: expert, column block, K block
   uint16_t* d;
@@ -70,35 +75,43 @@ struct ExpertParams {
   int* status;
 };
 
-template <bool PAIR_, bool F8_, ExpertMode MODE_>
+template <bool PAIR_, int BN_, bool F8_, ExpertMode MODE_>
 struct ExpertCfg {
-  static constexpr bool PAIR = PAIR_, F8 = F8_;
+  static constexpr bool PAIR = PAIR_, F8 = F8_, WIDE = BN_ == 256;
+  static_assert(WIDE || (BN_ == 128 && !PAIR), "tile widths");
   static constexpr ExpertMode MODE = MODE_;
   static constexpr bool DW = MODE == ExpertMode::Dw;
   static constexpr bool A_MN = DW, B_MN = MODE != ExpertMode::Fwd;
-  static constexpr int BM = PAIR ? 256 : 128, BN = PAIR ? 256 : 128;
+  static constexpr int BM = PAIR ? 256 : 128, BN = BN_;
+  static constexpr int BCTA = PAIR ? 128 : BN;          // columns of B that a CTA stages
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int BK = 128 / kElem;                // K per step: 128 bytes
-  static constexpr int kChunk = 128 / kElem;            // MN-major: columns per 128-byte row
-  static constexpr int kA = 128 * 128, kB = 128 * 128;  // bytes per CTA and stage
+  static constexpr int kChunk = 128 / kElem;            // MN-major: columns in 128 bytes
+  static constexpr int kA = 128 * 128, kB = BCTA * 128;  // bytes per CTA and stage
   static constexpr int kStage = kA + kB;
-  static constexpr int STAGES = PAIR ? 4 : 5;
-  static constexpr int kColGroups = BN / 64;
-  static constexpr int kEpiWarps = 4 * kColGroups;
-  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  static constexpr int STAGES = !PAIR && WIDE ? 3 : 5;
+  static constexpr int kCols = WIDE ? 128 : 64;         // columns per epilogue warp
+  static constexpr int kEpiWarps = 4 * (BN / kCols);
+  static constexpr int kThreads = (4 + kEpiWarps) * 32;
+  static constexpr int kRoleRegs = 56, kEpiRegs = 224;  // WIDE
+  static_assert(!WIDE || (kThreads == 384 && kRoleRegs * 128 + kEpiRegs * 256 <= 168 * 384), "register split");
   static constexpr int kTmemCols = 2 * BN;
-  static constexpr int kStaging = kEpiWarps * 4096;     // 32 rows x 128 bytes per warp
-  static constexpr int kBarOff = STAGES * kStage + kStaging;
-  static constexpr int kNumBars = 2 * STAGES + 6;
+  static constexpr int kPassCols = DW ? 32 : 64;        // D columns in 128 bytes
+  static constexpr int kStgBufs = 1;               // staging buffers per epilogue warp
+  static constexpr int kStaging = kEpiWarps * kStgBufs * 4096;   // 32 rows x 128 bytes each
+  static constexpr int kBlocksN = BN / 128;
+  static constexpr int kScaleSlots = 3;
+  static constexpr int kScaleSlot = 4 * kBlocksN * 512; // 4 steps x column blocks x 128 rows
+  static constexpr int kScaleOff = STAGES * kStage + kStaging;
+  static constexpr int kBarOff = kScaleOff + (F8 ? kScaleSlots * kScaleSlot : 0);
+  static constexpr int kNumBars = 2 * STAGES + 6 + 2 * kScaleSlots;
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kSmem = kTableOff + 2 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
 // acc += v * s for two values at once.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s2) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s2) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s2));
 }
 __device__ __forceinline__ uint64_t dup2(float s) {
@@ -117,8 +130,17 @@ struct ExpertTile {
   int k_row0, k_rows; // Dw: the group's rows
 };
 
-// Tiles run over an expert's row tiles first, then its column tiles, then the experts:
-// a column tile of the weight is shared by neighbours in time. `e` only moves up.
+// Within an expert tiles run in bands of kBand row tiles, over a band's rows first and then
+// the columns, so that the tiles in flight cover a near-square patch of D and share both
+// operands. `e` only moves up.
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_in_band(int r, int mt, int tiles_n, int& m, int& n) {
+  const int band = r / (kBand * tiles_n);
+  const int h = min(kBand, mt - band * kBand);
+  r -= band * kBand * tiles_n;
+  n = r / h;
+  m = band * kBand + r - n * h;
+}
 template <class C>
 __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, const int* starts, const int* tiles, int t,
                                                   int& e) {
@@ -126,9 +148,9 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, const i
   if constexpr (C::DW) {
     const int per = p.tiles_r * p.tiles_n;
     e = t / per;
-    const int r = t - e * per;
-    const int n = r / p.tiles_r;
-    x.row0 = (r - n * p.tiles_r) * C::BM;
+    int m, n;
+    tile_in_band(t - e * per, p.tiles_r, p.tiles_n, m, n);
+    x.row0 = m * C::BM;
     x.rows = p.d_rows - x.row0;
     x.n0 = n * C::BN;
     x.k_row0 = starts[e];
@@ -137,10 +159,8 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, const i
   } else {
     const int v = t / p.tiles_n;
     while (tiles[e + 1] <= v) ++e;
-    const int mt = tiles[e + 1] - tiles[e];
-    const int r = t - tiles[e] * p.tiles_n;
-    const int n = r / mt;
-    const int m = r - n * mt;
+    int m, n;
+    tile_in_band(t - tiles[e] * p.tiles_n, tiles[e + 1] - tiles[e], p.tiles_n, m, n);
     x.row0 = starts[e] + m * C::BM;
     x.rows = starts[e + 1] - x.row0;
     x.n0 = n * C::BN;
@@ -165,6 +185,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   auto tempty_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
   const uint32_t tail_bar = bars + 8u * (2 * C::STAGES + 4);
   const uint32_t drain_bar = bars + 8u * (2 * C::STAGES + 5);
+  auto sfull_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 6 + s); };
+  auto sempty_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 6 + C::kScaleSlots + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kNumBars);
   int* starts = reinterpret_cast<int*>(smem + C::kTableOff);
   int* tiles = starts + kMaxExperts + 1;
@@ -182,6 +204,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), (C::PAIR ? 2 : 1) * C::kEpiWarps);
+    }
+    if constexpr (C::F8) {
+      for (int s = 0; s < C::kScaleSlots; ++s) {
+        mbar_init(sfull_bar(s), 64);
+        mbar_init(sempty_bar(s), C::kEpiWarps);
+      }
     }
     mbar_init(tail_bar, 1);
     mbar_init(drain_bar, 1);
@@ -249,6 +277,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int num_tiles = C::DW ? p.E * p.tiles_r * p.tiles_n : tiles[p.E] * p.tiles_n;
   constexpr uint64_t kDrainNs = 100000000ull;
 
+  if (warp < 4) {
+  if constexpr (C::WIDE) regs_down<C::kRoleRegs>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -262,12 +292,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
       const int a_rows = min(128, max(0, x.rows - int(rank) * 128));
       const int boxes = C::A_MN || C::PAIR ? 1 : (a_rows + p.a_box - 1) / p.a_box;
-      const int b0 = x.n0 + int(rank) * 128;        // this CTA's columns of B
+      const int b0 = x.n0 + int(rank) * C::BCTA;    // this CTA's columns of B
       const int a0 = x.row0 + int(rank) * 128;      // this CTA's rows of D
       for (int kb = 0; kb < x.nk; ++kb, ++it) {
         const int s = it % C::STAGES;
         const uint32_t ph = (it / C::STAGES) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(s), ph ^ 1u))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_lazy(empty_bar(s), ph ^ 1u))) {
           if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 61);
           ok = false;
           break;
@@ -284,7 +314,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             // The even CTA's barrier counts both CTAs' bytes.
             bar = mapa_shared(full_bar(s), 0);
             if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * C::kStage);
-            else mbar_arrive_cluster(bar);
+            else mbar_arrive_remote(bar);
           } else {
             bar = full_bar(s);
             mbar_arrive_expect_tx(bar, (C::A_MN ? C::kA : boxes * p.a_box * 128) + C::kB);
@@ -300,30 +330,30 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           };
           if constexpr (C::DW) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              load2(a_s + c * 8192, &tmA, a0 + 64 * c, x.k_row0 + k0);
-              load2(b_s + c * 8192, &tmB, b0 + 64 * c, x.k_row0 + k0);
-            }
+            for (int c = 0; c < 2; ++c) load2(a_s + c * 8192, &tmA, a0 + 64 * c, x.k_row0 + k0);
+#pragma unroll
+            for (int c = 0; c < C::BCTA / 64; ++c) load2(b_s + c * 8192, &tmB, b0 + 64 * c, x.k_row0 + k0);
           } else {
             for (int b = 0; b < boxes; ++b) load2(a_s + b * p.a_box * 128, &tmA, k0, a0 + b * p.a_box);
             if constexpr (!C::B_MN) {
-              load3(b_s, &tmB, k0, b0);
+#pragma unroll
+              for (int c = 0; c < C::BCTA / 128; ++c) load3(b_s + c * 16384, &tmB, k0, b0 + c * 128);
             } else {
 #pragma unroll
-              for (int c = 0; c < 128 / C::kChunk; ++c)
+              for (int c = 0; c < C::BCTA / C::kChunk; ++c)
                 load3(b_s + c * C::BK * 128, &tmB, b0 + c * C::kChunk, k0);
             }
           }
         }
         if (tail) {
-          if (!__all_sync(0xffffffffu, mbar_wait(tail_bar, ntail & 1u))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_lazy(tail_bar, ntail & 1u))) {
             if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 62);
             ok = false;
             break;
           }
           ++ntail;
           const uint4 z = make_uint4(0, 0, 0, 0);
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < C::kStage / 8192; ++c) {
             uint8_t* chunk = smem + s * C::kStage + c * 8192;
             for (int i = valid * 8 + int(lane); i < 512; i += 32) reinterpret_cast<uint4*>(chunk)[i] = z;
           }
@@ -341,7 +371,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (!ok && it > 0 && rank == 0) {
       for (uint32_t k = 0; k < uint32_t(C::STAGES) && k < it; ++k) {
         const uint32_t i2 = it - 1 - k;
-        mbar_wait(full_bar(i2 % C::STAGES), (i2 / C::STAGES) & 1u, kDrainNs);
+        mbar_wait_lazy(full_bar(i2 % C::STAGES), (i2 / C::STAGES) & 1u, kDrainNs);
       }
     }
   } else if (warp == 1) {
@@ -363,8 +393,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int kb = 0; kb < x.nk; ++kb, ++it) {
           const uint32_t buf = u & 1u;
           if (C::F8 || kb == 0) {
-            if (!(C::PAIR ? mbar_wait_cluster(tempty_bar(buf), ((u >> 1) & 1u) ^ 1u)
-                          : mbar_wait(tempty_bar(buf), ((u >> 1) & 1u) ^ 1u))) {
+            if (!mbar_wait_lazy(tempty_bar(buf), ((u >> 1) & 1u) ^ 1u)) {
               set_status_site(p.status, QLORA_ERR_TIMEOUT, 63);
               ok = false;
               break;
@@ -372,7 +401,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           const int s = it % C::STAGES;
           const uint32_t ph = (it / C::STAGES) & 1u;
-          if (!(C::PAIR ? mbar_wait_cluster(full_bar(s), ph) : mbar_wait(full_bar(s), ph))) {
+          // (cluster scope where the other CTA's generic stores, a cleared tail, are handed over)
+          const bool tail = C::PAIR && C::DW && x.k_rows - kb * C::BK < C::BK;
+          if (!(tail ? mbar_wait_cluster(full_bar(s), ph) : mbar_wait_lazy(full_bar(s), ph))) {
             set_status_site(p.status, QLORA_ERR_TIMEOUT, 64);
             ok = false;
             break;
@@ -406,71 +437,138 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       // All MMAs of this thread are complete once drain_bar flips.
       if constexpr (C::PAIR) tc_commit_pair_mc(drain_bar, 1);
       else tc_commit(drain_bar);
-      mbar_wait(drain_bar, 0, kDrainNs);
+      mbar_wait_lazy(drain_bar, 0, kDrainNs);
     }
   } else {
+    // ------------------------------------------------------------ scales
+    // The products sa sb of the tile's 128 rows and column blocks, four steps at a time, two
+    // rows a thread. Rows past the group's end take its last row's scales (in bounds; their
+    // products are not stored), steps past the last one take its.
+    if constexpr (C::F8) {
+      const int t0 = int(threadIdx.x) - 64;
+      uint32_t g = 0;
+      int e = 0;
+      bool ok = true;
+      for (int t = unit; t < num_tiles && ok; t += units) {
+        const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
+        const int r0 = int(rank) * 128 + t0;
+        const float* ra = p.sa + int64_t(x.row0 + min(r0, x.rows - 1)) * p.nb_a;
+        const float* rb = p.sa + int64_t(x.row0 + min(r0 + 64, x.rows - 1)) * p.nb_a;
+        const float* sb = p.sb + x.e * p.sb_e;
+        for (int k0 = 0; k0 < x.nk; k0 += 4, ++g) {
+          const int s = g % C::kScaleSlots;
+          float a[2][4], w[C::kBlocksN][4];
+          if (p.sa_vec) {
+            const float4 u = __ldg(reinterpret_cast<const float4*>(ra + k0));
+            const float4 v = __ldg(reinterpret_cast<const float4*>(rb + k0));
+            a[0][0] = u.x; a[0][1] = u.y; a[0][2] = u.z; a[0][3] = u.w;
+            a[1][0] = v.x; a[1][1] = v.y; a[1][2] = v.z; a[1][3] = v.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              a[0][j] = __ldg(ra + min(k0 + j, x.nk - 1));
+              a[1][j] = __ldg(rb + min(k0 + j, x.nk - 1));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < C::kBlocksN; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[b][j] = __ldg(sb + min((x.n0 >> 7) + b, p.nb_n - 1) * p.sb_n + min(k0 + j, x.nk - 1) * p.sb_k);
+          if (!__all_sync(0xffffffffu, mbar_wait_lazy(sempty_bar(s), ((g / C::kScaleSlots) & 1u) ^ 1u))) {
+            if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 66);
+            ok = false;
+            break;
+          }
+          float* dst = reinterpret_cast<float*>(smem + C::kScaleOff + s * C::kScaleSlot) + t0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int b = 0; b < C::kBlocksN; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) dst[(j * C::kBlocksN + b) * 128 + 64 * h] = a[h][j] * w[b][j];
+          mbar_arrive(sfull_bar(s));
+        }
+      }
+    }
+  }
+  } else {
     // ------------------------------------------------------------ epilogue
+    if constexpr (C::WIDE) regs_up<C::kEpiRegs>();
     const uint32_t q = warp & 3u;                 // TMEM lane quadrant this warp may read
-    const int cg = int(warp - 2) >> 2;            // 64-column group
-    const uint32_t stage_off = C::STAGES * C::kStage + (warp - 2) * 4096u;
-    const uint32_t stg = base + stage_off;
-    const uint32_t trow = tmem + ((q * 32u) << 16) + cg * 64;
-    uint32_t u = 0;
+    const int cg = int(warp - 4) >> 2;            // column group
+    const uint32_t stg0 = base + C::STAGES * C::kStage + (warp - 4) * (C::kStgBufs * 4096u);
+    const uint32_t trow = tmem + ((q * 32u) << 16) + cg * C::kCols;
+    uint32_t npass = 0;
+    uint32_t u = 0, g = 0;
     int e = 0;
     bool ok = true;
     for (int t = unit; t < num_tiles && ok; t += units) {
       const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
       const int first = int(rank) * 128 + int(q) * 32;       // this warp's first row in the tile
       const int rows = min(32, x.rows - first);              // rows to store (may be <= 0)
-      const int col0 = x.n0 + cg * 64;
-      uint64_t acc[32];
+      const int col0 = x.n0 + cg * C::kCols;
+      uint64_t acc[C::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = 0;
-      const float* sa = nullptr;
-      const float* sb = nullptr;
-      float s_next = 0.f;
-      if constexpr (C::F8) {
-        sa = p.sa + int64_t(x.row0 + first + min(int(lane), max(rows, 1) - 1)) * p.nb_a;
-        sb = p.sb + x.e * p.sb_e + min(col0 >> 7, p.nb_n - 1) * p.sb_n;
-        if (rows > 0) s_next = __ldg(sa) * __ldg(sb);
-      }
-      const int reads = C::F8 ? x.nk : (x.nk > 0 ? 1 : 0);
-      for (int k = 0; k < reads; ++k, ++u) {
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
+      // Adds s times the next TMEM buffer to acc, and hands the buffer back.
+      auto take = [&](float s) {
         const uint32_t buf = u & 1u;
-        const float s = s_next;
-        if (C::F8 && k + 1 < reads && rows > 0) s_next = __ldg(sa + k + 1) * __ldg(sb + (k + 1) * p.sb_k);
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), (u >> 1) & 1u))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_lazy(tfull_bar(buf), (u >> 1) & 1u))) {
           if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 65);
-          ok = false;
-          break;
+          ok = false;   // (and on, so that the sums have one path: they are not stored)
         }
+        ++u;
         tc_fence_after();
-        const uint64_t s2 = dup2(C::F8 ? s : 1.f);
+        const uint64_t s2 = dup2(s);
+        constexpr int kLoads = C::kCols / 64;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(trow + buf * C::BN + h * 32, v);
+        for (int c = 0; c < kLoads; ++c) {
+          uint64_t v[32];
+          tmem_ld_32x32b_x64_pairs(trow + buf * C::BN + c * 64, v);
           tmem_ld_wait_for(v);
-          if (h == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (C::PAIR) mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
-              else mbar_arrive(tempty_bar(buf));
-            }
+          if (c + 1 == kLoads) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (C::PAIR) mbar_arrive_remote(mapa_shared(tempty_bar(buf), 0));
+                else mbar_arrive(tempty_bar(buf));
+              }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(acc[h * 16 + i], v[2 * i], v[2 * i + 1], s2);
+          for (int i = 0; i < 32; ++i) fma2(acc[c * 32 + i], v[i], s2);
         }
+      };
+      if constexpr (C::F8) {
+        for (int k = 0; k < x.nk && ok; ++k) {
+          const uint32_t slot = g % C::kScaleSlots;
+          if (k % 4 == 0 && !__all_sync(0xffffffffu, mbar_wait_lazy(sfull_bar(slot), (g / C::kScaleSlots) & 1u))) {
+            if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 67);
+            ok = false;
+          }
+          const float f = reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScaleSlot)
+              [((k & 3) * C::kBlocksN + cg * C::kCols / 128) * 128 + q * 32 + lane];
+          take(f);
+          if (k % 4 == 3 || k == x.nk - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sempty_bar(slot));
+            ++g;
+          }
+        }
+      } else {
+        if (x.nk > 0) take(1.f);
       }
       if (!ok) break;
-      if (rows <= 0 || col0 >= p.n_cols) continue;
-      // Through this warp's staging rows (128-byte swizzle) to global memory: by TMA, or row
+      if (rows <= 0) continue;
+      // Through this warp's staging buffers (128-byte swizzle) to global memory: by TMA, or row
       // by row where the group ends inside the 32 rows.
-      constexpr int kPasses = C::DW ? 2 : 1;
+      const int row = x.row0 + first;
 #pragma unroll
-      for (int ps = 0; ps < kPasses; ++ps) {
-        if (lane == 0) bulk_wait_group_read<0>();
+      for (int ps = 0; ps < C::kCols / C::kPassCols; ++ps) {
+        const int col = col0 + ps * C::kPassCols;
+        if (col >= p.n_cols) break;
+        const uint32_t stg = stg0 + (npass++ % C::kStgBufs) * 4096u;
+        if (lane == 0) bulk_wait_group_read<C::kStgBufs - 1>();
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -481,27 +579,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           } else {
             uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack2(acc[4 * c + i], w[2 * i], w[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) unpack2(acc[ps * 32 + 4 * c + i], w[2 * i], w[2 * i + 1]);
             o.x = pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1]));
             o.y = pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3]));
             o.z = pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5]));
             o.w = pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7]));
           }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128u + ((uint32_t(c) ^ (lane & 7u)) << 4)),
-                       "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
-                       : "memory");
+          sts_u4(stg + lane * 128u + ((uint32_t(c) ^ (lane & 7u)) << 4), o);
         }
-        const int row = x.row0 + first;
         if (C::DW || rows == 32) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if constexpr (C::DW) {
-              if (col0 + 32 * ps < p.n_cols) tma_store_3d(&tmD, stg, col0 + 32 * ps, row, x.e);
-            } else {
-              tma_store_2d(&tmD, stg, col0, row);
-            }
-            bulk_commit_group();
+            if constexpr (C::DW) tma_store_3d(&tmD, stg, col, row, x.e);
+            else tma_store_2d(&tmD, stg, col, row);
           }
         } else {
           __syncwarp();
@@ -510,12 +601,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const int r = i * 4 + int(lane >> 3), c = int(lane & 7u);
             uint32_t v[4];
             lds_u4(stg + r * 128u + ((uint32_t(c) ^ (r & 7u)) << 4), v);
-            if (r < rows && col0 + c * 8 < p.n_cols)
-              *reinterpret_cast<uint4*>(p.d + int64_t(row + r) * p.ld_d + col0 + c * 8) =
+            if (r < rows && col + c * 8 < p.n_cols)
+              *reinterpret_cast<uint4*>(p.d + int64_t(row + r) * p.ld_d + col + c * 8) =
                   make_uint4(v[0], v[1], v[2], v[3]);
           }
-          __syncwarp();
         }
+        // (a group for every buffer, empty after plain stores, so that the wait above counts)
+        if (lane == 0) bulk_commit_group();
       }
     }
     if (lane == 0) bulk_wait_group<0>();
@@ -594,6 +686,7 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
   p.sa = a.sa;
   p.sb = a.sb;
   p.nb_a = int((K + 127) / 128);
+  p.sa_vec = p.nb_a % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sa) & 15u) == 0;
   p.nb_n = int((N + 127) / 128);
   const int64_t nbo = (a.out + 127) / 128, nbi = (a.in + 127) / 128;
   p.sb_e = nbo * nbi;
@@ -649,14 +742,20 @@ qlora_status launch_mode(const ExpertArgs& a, cudaStream_t s) {
   // Pair tiles halve the L2 bytes per product; single tiles waste fewer rows of small groups.
   const int64_t N = MODE == ExpertMode::Fwd ? a.out : a.in;
   const int64_t rows = MODE == ExpertMode::Dw ? a.out : a.M / a.E;
-  const bool pair = rows >= 192 && N >= 256;
-  if (pair) return launch_cfg<ExpertCfg<true, F8, MODE>>(a, s);
-  return launch_cfg<ExpertCfg<false, F8, MODE>>(a, s);
+  bool pair = rows >= 192 && N >= 256;
+  const char* f = std::getenv("QLB_FORCE");
+  const int force = f ? std::atoi(f) : 0;
+  if (force == 1) return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
+  if (force == 2) return launch_cfg<ExpertCfg<false, 256, F8, MODE>>(a, s);
+  if (force == 3) return launch_cfg<ExpertCfg<true, 256, F8, MODE>>(a, s);
+  if (pair) return launch_cfg<ExpertCfg<true, 256, F8, MODE>>(a, s);
+  return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
 }
 
 }  // namespace
 
 qlora_status launch_expert_gemm(const ExpertArgs& a, cudaStream_t s) {
+  if (few_rows_wanted(a)) return launch_few_rows(a, false, s);
   switch (a.mode) {
     case ExpertMode::Fwd:
       return a.f8 ? launch_mode<true, ExpertMode::Fwd>(a, s) : launch_mode<false, ExpertMode::Fwd>(a, s);

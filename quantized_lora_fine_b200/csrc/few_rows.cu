@@ -1,0 +1,251 @@
+// Y_e = X_e W_e^T for few rows a group (decoding): bound by reading the weights once.
+//
+// A CTA takes 16 rows of one expert's weight over all of K, its 8 warps every eighth
+// 128-byte block of K. The rows stream from global memory into the registers of
+// mma.sync fragments: lane (g, t) loads 32 neighbouring bytes of weight rows g and
+// g + 8, and the same 32 bytes of token g, and gives their words to four products in
+// the same order on both sides (a sum over k may run over k in any order), so every load
+// is 16 bytes wide and nothing passes through shared memory. Weight rows are the
+// product's 16 rows, tokens its 8 columns. In e4m3 a block's product is scaled by sa sb
+// and added in fp32; the warps' sums are added in order at the end.
+//
+// With bf16 rows and an e4m3 weight (QUANT, up to 8 rows in all) each warp quantizes the
+// blocks that it multiplies, as quantize_rows8_kernel does, which saves that launch.
+//
+// tcgen05 tiles of 128 rows would leave most SMs without a tile here: 4096 x 4096 has 32.
+#include <algorithm>
+
+#include "block8.cuh"
+#include "expert_gemm.cuh"
+#include "internal.cuh"
+#include "nf4_device.cuh"
+#include "ptx.cuh"
+
+namespace qlb {
+
+namespace {
+
+struct FewParams {
+  const uint8_t* w;      // [E][out][wbytes]
+  const uint8_t* x;      // [M][wbytes], or bf16 [M][in] with QUANT
+  const float* sa;
+  const float* sb;
+  const int32_t* offsets;
+  uint16_t* y;
+  int* status;
+  int M, E, out, in;
+  int wbytes;            // bytes of a weight row
+  int nk;                // 128-byte blocks of K
+  int nb_n;              // scale rows per expert
+};
+
+constexpr int kFewWarps = 8;
+
+template <bool F8>
+__device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  if constexpr (F8) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// 32 bytes at p; zero where the row ends (at a multiple of 16).
+__device__ __forceinline__ void load32(uint32_t (&v)[8], const uint8_t* p, int left) {
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const uint4 a = left >= 16 ? __ldg(reinterpret_cast<const uint4*>(p)) : z;
+  const uint4 b = left >= 32 ? __ldg(reinterpret_cast<const uint4*>(p) + 1) : z;
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+// Weights are read once: not kept in L1.
+__device__ __forceinline__ void stream32(uint32_t (&v)[8], const uint8_t* p, int left) {
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const uint4 a = left >= 16 ? __ldcs(reinterpret_cast<const uint4*>(p)) : z;
+  const uint4 b = left >= 32 ? __ldcs(reinterpret_cast<const uint4*>(p) + 1) : z;
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// NT: 8-token columns a pass; U: blocks of K in flight a warp.
+template <bool F8, int NT, int U, bool QUANT>
+__global__ void __launch_bounds__(kFewWarps * 32) few_rows_kernel(const FewParams p) {
+  static_assert(!QUANT || (F8 && NT == 1), "rows quantized here are at most 8, in e4m3");
+  __shared__ float red[kFewWarps][NT * 8][17];
+  __shared__ __align__(16) uint8_t xq[QUANT ? kFewWarps * U * 8 * 128 : 16];
+  __shared__ float xs[QUANT ? kFewWarps * U * 8 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int e = blockIdx.y, n0 = blockIdx.x * 16;
+  pdl_wait();
+  pdl_launch();
+  // The group's rows: the running maximum of the offsets clamped to [0, M], as the tiled kernel.
+  int first = 0, last = p.M;
+  if (p.offsets) {
+    int v = 0;
+    for (int i = lane; i <= e; i += 32) v = max(v, __ldg(p.offsets + i));
+    const int r0 = __ldg(p.offsets + e), r1 = __ldg(p.offsets + e + 1);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+    first = min(v, p.M);
+    last = max(first, min(max(r1, 0), p.M));
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (r0 < 0 || r1 > p.M || r1 < r0))
+      set_status_site(p.status, QLORA_ERR_SHAPE, 70);
+  }
+  const uint8_t* w0 = p.w + (int64_t(e) * p.out + n0 + g) * p.wbytes + 32 * t;
+  const uint8_t* w1 = w0 + int64_t(8) * p.wbytes;
+  const float* sb = F8 ? p.sb + (int64_t(e) * p.nb_n + (n0 >> 7)) * p.nk : nullptr;
+
+  for (int m0 = first; m0 < last; m0 += NT * 8) {
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    for (int k0 = warp; k0 < p.nk; k0 += kFewWarps * U) {
+      uint32_t a[U][2][8], b[U][NT][8];
+      float f[U][NT][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * kFewWarps;
+        const int left = k < p.nk ? p.wbytes - k * 128 - 32 * t : 0;
+        stream32(a[u][0], w0 + int64_t(k) * 128, left);
+        stream32(a[u][1], w1 + int64_t(k) * 128, left);
+      }
+      if constexpr (QUANT) {
+        uint8_t* xw = xq + warp * U * 8 * 128;
+        float* sw = xs + warp * U * 8;
+        __syncwarp();
+        for (int m = 0; m < last - m0; ++m) {      // at most 8 rows
+          uint2 v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int col = (k0 + u * kFewWarps) * 128 + lane * 4;
+            v[u] = col < p.in ? __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.x) +
+                                                                     int64_t(m0 + m) * p.in + col))
+                              : make_uint2(0, 0);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float q0 = __uint_as_float(v[u].x << 16), q1 = __uint_as_float(v[u].x & 0xFFFF0000u);
+            const float q2 = __uint_as_float(v[u].y << 16), q3 = __uint_as_float(v[u].y & 0xFFFF0000u);
+            uint32_t mx = max(max(v[u].x & 0x7FFFu, (v[u].x >> 16) & 0x7FFFu),
+                              max(v[u].y & 0x7FFFu, (v[u].y >> 16) & 0x7FFFu)) << 16;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const Block8 q = block8_of(mx);
+            reinterpret_cast<uint32_t*>(xw + (u * 8 + m) * 128)[lane] =
+                e4m3x4(block8_quotient(q0, q), block8_quotient(q1, q), block8_quotient(q2, q), block8_quotient(q3, q));
+            if (lane == 0) sw[u * 8 + m] = q.scale;
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * kFewWarps;
+        const int left = k < p.nk ? p.wbytes - k * 128 - 32 * t : 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int m = m0 + n * 8 + g;
+          if constexpr (QUANT) {
+            const uint8_t* src = xq + ((warp * U + u) * 8 + g) * 128 + 32 * t;
+            const bool live = m < last && k < p.nk;
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            const uint4 lo = live ? reinterpret_cast<const uint4*>(src)[0] : z;
+            const uint4 hi = live ? reinterpret_cast<const uint4*>(src)[1] : z;
+            b[u][n][0] = lo.x; b[u][n][1] = lo.y; b[u][n][2] = lo.z; b[u][n][3] = lo.w;
+            b[u][n][4] = hi.x; b[u][n][5] = hi.y; b[u][n][6] = hi.z; b[u][n][7] = hi.w;
+          } else {
+            load32(b[u][n], p.x + int64_t(m) * p.wbytes + k * 128 + 32 * t, m < last ? left : 0);
+          }
+          if constexpr (F8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = m0 + n * 8 + 2 * t + h;
+              f[u][n][h] = 0.f;
+              if (c < last && k < p.nk) {
+                if constexpr (QUANT) f[u][n][h] = xs[(warp * U + u) * 8 + 2 * t + h] * __ldg(sb + k);
+                else f[u][n][h] = __ldg(p.sa + int64_t(c) * p.nk + k) * __ldg(sb + k);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (F8) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma16x8<F8>(c, a[u][0][2 * j], a[u][1][2 * j], a[u][0][2 * j + 1], a[u][1][2 * j + 1], b[u][n][2 * j],
+                          b[u][n][2 * j + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(c[i], f[u][n][i & 1], acc[n][i]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma16x8<F8>(acc[n], a[u][0][2 * j], a[u][1][2 * j], a[u][0][2 * j + 1], a[u][1][2 * j + 1],
+                          b[u][n][2 * j], b[u][n][2 * j + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[warp][n * 8 + 2 * t + (i & 1)][g + (i >> 1) * 8] = acc[n][i];
+    __syncthreads();
+    const int r = threadIdx.x & 15, m = threadIdx.x >> 4;
+    if (m < NT * 8 && m0 + m < last) {
+      float s = red[0][m][r];
+#pragma unroll
+      for (int k = 1; k < kFewWarps; ++k) s += red[k][m][r];
+      p.y[int64_t(m0 + m) * p.out + n0 + r] = uint16_t(pack_bf16x2(s, s) & 0xFFFFu);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+// Rows that a group has on average, up to which this kernel is taken.
+bool few_rows_wanted(const ExpertArgs& a) { return a.mode == ExpertMode::Fwd && a.M <= 16 * a.E; }
+
+qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s) {
+  FewParams p = {};
+  p.w = static_cast<const uint8_t*>(a.b);
+  p.x = static_cast<const uint8_t*>(a.a);
+  p.sa = a.sa;
+  p.sb = a.sb;
+  p.offsets = a.offsets;
+  p.y = static_cast<uint16_t*>(a.d);
+  p.status = a.status;
+  p.M = int(a.M);
+  p.E = int(a.E);
+  p.out = int(a.out);
+  p.in = int(a.in);
+  p.wbytes = int(a.in) * (a.f8 ? 1 : 2);
+  p.nk = (p.wbytes + 127) / 128;
+  p.nb_n = int((a.out + 127) / 128);
+  const dim3 grid(unsigned(a.out / 16), unsigned(a.E)), block(kFewWarps * 32);
+  const bool two = !quantize && a.M > 4 * a.E && a.M > 8;
+  cudaError_t r;
+  if (quantize) r = launch_pdl(few_rows_kernel<true, 1, 4, true>, grid, block, 0, s, p);
+  else if (a.f8) r = two ? launch_pdl(few_rows_kernel<true, 2, 2, false>, grid, block, 0, s, p)
+                         : launch_pdl(few_rows_kernel<true, 1, 4, false>, grid, block, 0, s, p);
+  else r = two ? launch_pdl(few_rows_kernel<false, 2, 2, false>, grid, block, 0, s, p)
+               : launch_pdl(few_rows_kernel<false, 1, 4, false>, grid, block, 0, s, p);
+  return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);
+}
+
+}  // namespace qlb

@@ -19,12 +19,14 @@
 // feeds twice the products that it does in a 128 x 128 tile). Roles:
 //   warp 0      TMA producer
 //   warp 1      TMEM allocation, MMA issue (even CTA of a pair)
-//   warps 2, 3  (e4m3 only) scales of A's rows to shared memory, four steps at a time
+//   warps 2, 3  e4m3: products of the scales to shared memory, four steps at a time;
+//               Dw: ends of groups
 //   warps 4..   epilogue, 4 lane quadrants x column groups: each warp owns 32 rows x 128
-//               columns (64 in single tiles), in registers
-// In a pair a thread holds 128 sums and 32 values in flight; the first warpgroup gives up
-// registers for that (168 x 384 = 88 x 128 + 208 x 256). 16 epilogue warps of 64 columns
-// have 96 registers at most and spill.
+//               columns (64 in 128-column tiles), in registers
+// In 256-column tiles an epilogue thread holds 128 sums and 64 values in flight; the first
+// warpgroup gives up registers for that (168 x 384 = 56 x 128 + 224 x 256). 16 epilogue
+// warps of 64 columns have 96 registers at most and spill: the e4m3 forward at 8192 x 11008
+// x 4096 took 567 us with them and takes 376.
 // Stage: 128 rows (or columns) x 128 bytes of K for each operand, 128-byte swizzle,
 // K-major as stored along K, MN-major where the reduction runs over rows.
 //
@@ -104,7 +106,7 @@ struct ExpertCfg {
   static constexpr int kScaleSlot = 4 * kBlocksN * 512; // 4 steps x column blocks x 128 rows
   static constexpr int kScaleOff = STAGES * kStage + kStaging;
   static constexpr int kBarOff = kScaleOff + (F8 ? kScaleSlots * kScaleSlot : 0);
-  static constexpr int kNumBars = 2 * STAGES + 6 + 2 * kScaleSlots;
+  static constexpr int kNumBars = 3 * STAGES + 5 + 2 * kScaleSlots;
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kSmem = kTableOff + 2 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -183,10 +185,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
   auto tfull_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
   auto tempty_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
-  const uint32_t tail_bar = bars + 8u * (2 * C::STAGES + 4);
-  const uint32_t drain_bar = bars + 8u * (2 * C::STAGES + 5);
-  auto sfull_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 6 + s); };
-  auto sempty_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 6 + C::kScaleSlots + s); };
+  auto tail_bar = [&](int i) { return bars + 8u * (2 * C::STAGES + 4 + i); };
+  const uint32_t drain_bar = bars + 8u * (3 * C::STAGES + 4);
+  auto sfull_bar = [&](int s) { return bars + 8u * (3 * C::STAGES + 5 + s); };
+  auto sempty_bar = [&](int s) { return bars + 8u * (3 * C::STAGES + 5 + C::kScaleSlots + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kNumBars);
   int* starts = reinterpret_cast<int*>(smem + C::kTableOff);
   int* tiles = starts + kMaxExperts + 1;
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         mbar_init(sempty_bar(s), C::kEpiWarps);
       }
     }
-    mbar_init(tail_bar, 1);
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(tail_bar(s), 1);
     mbar_init(drain_bar, 1);
     fence_mbarrier_init();
     fence_proxy_async_smem();
@@ -308,7 +310,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (lane == 0) {
           uint32_t bar;
           if (tail) {
-            bar = tail_bar;
+            // landed on a barrier of its own, which warp 2 waits on; it hands the stage over
+            bar = tail_bar(ntail % C::STAGES);
             mbar_arrive_expect_tx(bar, C::kStage);
           } else if constexpr (C::PAIR) {
             // The even CTA's barrier counts both CTAs' bytes.
@@ -345,25 +348,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
           }
         }
-        if (tail) {
-          if (!__all_sync(0xffffffffu, mbar_wait_lazy(tail_bar, ntail & 1u))) {
-            if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 62);
-            ok = false;
-            break;
-          }
-          ++ntail;
-          const uint4 z = make_uint4(0, 0, 0, 0);
-          for (int c = 0; c < C::kStage / 8192; ++c) {
-            uint8_t* chunk = smem + s * C::kStage + c * 8192;
-            for (int i = valid * 8 + int(lane); i < 512; i += 32) reinterpret_cast<uint4*>(chunk)[i] = z;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (C::PAIR) mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
-            else mbar_arrive(full_bar(s));
-          }
-        }
+        if (tail) ++ntail;
         __syncwarp();
       }
     }
@@ -438,6 +423,36 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if constexpr (C::PAIR) tc_commit_pair_mc(drain_bar, 1);
       else tc_commit(drain_bar);
       mbar_wait_lazy(drain_bar, 0, kDrainNs);
+    }
+  } else if (C::DW && warp == 2) {
+    // ------------------------------------------------------------ ends of groups
+    // Clears the last step of a group past its last row in both operands. (In the producer
+    // the wait for the step's copies held up the next tile's: every group has such a step,
+    // and with 256 rows a group it is one in five.)
+    uint32_t it = 0, ntail = 0;
+    int e = 0;
+    for (int t = unit; t < num_tiles; t += units) {
+      const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
+      it += x.nk;
+      const int valid = x.k_rows - (x.nk - 1) * C::BK;
+      if (x.nk == 0 || valid == C::BK) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait_lazy(tail_bar(ntail % C::STAGES), (ntail / C::STAGES) & 1u))) {
+        if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 62);
+        break;
+      }
+      ++ntail;
+      const int s = (it - 1) % C::STAGES;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < C::kStage / 8192; ++c) {
+        uint8_t* chunk = smem + s * C::kStage + c * 8192;
+        for (int i = valid * 8 + int(lane); i < 512; i += 32) reinterpret_cast<uint4*>(chunk)[i] = z;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (C::PAIR) mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
+        else mbar_arrive(full_bar(s));
+      }
     }
   } else {
     // ------------------------------------------------------------ scales
@@ -737,19 +752,54 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
   return QLORA_OK;
 }
 
+// The tile: by the time that the waves of tiles take, a wave's steps at the rates measured
+// with full waves (us per step of 128 bytes of K):
+//                  e4m3    bf16
+//   128 x 128      0.47    0.40     148 at once; the most units and the fewest wasted rows
+//   128 x 256      0.65    0.48     148 at once
+//   256 x 256 pair 0.62    0.44     74 at once; half the L2 bytes of 128 x 128 per product
+// (e4m3 4096 x 4096 at 512 rows: 18.5, 21.8 and 22.0 us; at 768: 32.1, 22.7 and 22.6; at
+// 8192: 202, 143 and 137.) The row tiles of groups, whose sizes are on the device, are taken as
+// half a tile more than full for each group. Dw, which writes fp32 and has few steps a tile,
+// by the waves alone (16 experts of 1408 x 2048, 512 rows each: 84, 79 and 82 us, waves of 20,
+// 10 and 11; 64 of 1024 x 2048, 64 rows each: 116, 112 and 98 us, 28 waves of either).
+// QLORA_B200_EXPERT_TILE=128|256|pair overrides the choice, for measurement and tests.
+enum class ExpertTileKind { T128, T256, Pair };
+template <bool F8>
+ExpertTileKind tile_kind(const ExpertArgs& a) {
+  const char* f = std::getenv("QLORA_B200_EXPERT_TILE");
+  if (f) {
+    if (std::strcmp(f, "128") == 0) return ExpertTileKind::T128;
+    if (std::strcmp(f, "256") == 0) return ExpertTileKind::T256;
+    if (std::strcmp(f, "pair") == 0) return ExpertTileKind::Pair;
+  }
+  if (a.mode == ExpertMode::Dw) {
+    if (a.in <= 128) return ExpertTileKind::T128;
+    auto waves = [&](int bm, int at_once) {
+      return (a.E * ((a.out + bm - 1) / bm) * ((a.in + 255) / 256) + at_once - 1) / at_once;
+    };
+    return waves(256, 74) <= waves(128, 148) ? ExpertTileKind::Pair : ExpertTileKind::T256;
+  }
+  const int64_t N = a.mode == ExpertMode::Fwd ? a.out : a.in;
+  auto cost = [&](int bm, int bn, int at_once, double step) {
+    int64_t rt = (a.M + bm - 1) / bm;
+    if (a.offsets) rt = std::max(std::min(a.E, a.M), a.M / bm + a.E / 2);
+    const int64_t tiles = rt * ((N + bn - 1) / bn);
+    return double((tiles + at_once - 1) / at_once) * step;
+  };
+  const double c128 = cost(128, 128, 148, F8 ? 0.47 : 0.40), c256 = cost(128, 256, 148, F8 ? 0.65 : 0.48),
+               cpair = cost(256, 256, 74, F8 ? 0.62 : 0.44);
+  if (cpair <= c256 && cpair <= c128) return ExpertTileKind::Pair;
+  return c256 <= c128 ? ExpertTileKind::T256 : ExpertTileKind::T128;
+}
+
 template <bool F8, ExpertMode MODE>
 qlora_status launch_mode(const ExpertArgs& a, cudaStream_t s) {
-  // Pair tiles halve the L2 bytes per product; single tiles waste fewer rows of small groups.
-  const int64_t N = MODE == ExpertMode::Fwd ? a.out : a.in;
-  const int64_t rows = MODE == ExpertMode::Dw ? a.out : a.M / a.E;
-  bool pair = rows >= 192 && N >= 256;
-  const char* f = std::getenv("QLB_FORCE");
-  const int force = f ? std::atoi(f) : 0;
-  if (force == 1) return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
-  if (force == 2) return launch_cfg<ExpertCfg<false, 256, F8, MODE>>(a, s);
-  if (force == 3) return launch_cfg<ExpertCfg<true, 256, F8, MODE>>(a, s);
-  if (pair) return launch_cfg<ExpertCfg<true, 256, F8, MODE>>(a, s);
-  return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
+  switch (tile_kind<F8>(a)) {
+    case ExpertTileKind::Pair: return launch_cfg<ExpertCfg<true, 256, F8, MODE>>(a, s);
+    case ExpertTileKind::T256: return launch_cfg<ExpertCfg<false, 256, F8, MODE>>(a, s);
+    default: return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
+  }
 }
 
 }  // namespace

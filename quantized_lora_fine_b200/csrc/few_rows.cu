@@ -14,6 +14,7 @@
 //
 // tcgen05 tiles of 128 rows would leave most SMs without a tile here: 4096 x 4096 has 32.
 #include <algorithm>
+#include <cstdlib>
 
 #include "block8.cuh"
 #include "expert_gemm.cuh"
@@ -76,7 +77,7 @@ __device__ __forceinline__ void stream32(uint32_t (&v)[8], const uint8_t* p, int
 
 // NT: 8-token columns a pass; U: blocks of K in flight a warp.
 template <bool F8, int NT, int U, bool QUANT>
-__global__ void __launch_bounds__(kFewWarps * 32) few_rows_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kFewWarps * 32, (F8 && !QUANT && NT == 1) ? 4 : 2) few_rows_kernel(const FewParams p) {
   static_assert(!QUANT || (F8 && NT == 1), "rows quantized here are at most 8, in e4m3");
   __shared__ float red[kFewWarps][NT * 8][17];
   __shared__ __align__(16) uint8_t xq[QUANT ? kFewWarps * U * 8 * 128 : 16];
@@ -218,8 +219,14 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_rows_kernel(const FewParam
 
 }  // namespace
 
-// Rows that a group has on average, up to which this kernel is taken.
-bool few_rows_wanted(const ExpertArgs& a) { return a.mode == ExpertMode::Fwd && a.M <= 16 * a.E; }
+// Up to 16 rows of one group, or 2 a group on average (more rows are right, pass by pass,
+// but each pass fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 6.7 us against 16.6
+// with tiles; 64 experts of 1024 x 2048 in bf16: 32 us against 37 at one row a group, 47.5
+// against 49 at four, 80 against 50 at sixteen. QLORA_B200_EXPERT_TILE set: never.
+bool few_rows_wanted(const ExpertArgs& a) {
+  if (a.mode != ExpertMode::Fwd || std::getenv("QLORA_B200_EXPERT_TILE")) return false;
+  return a.offsets ? a.M <= 2 * a.E : a.M <= 16;
+}
 
 qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s) {
   FewParams p = {};
@@ -238,11 +245,11 @@ qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s)
   p.nk = (p.wbytes + 127) / 128;
   p.nb_n = int((a.out + 127) / 128);
   const dim3 grid(unsigned(a.out / 16), unsigned(a.E)), block(kFewWarps * 32);
-  const bool two = !quantize && a.M > 4 * a.E && a.M > 8;
+  const bool two = !quantize && !a.offsets && a.M > 8;
   cudaError_t r;
   if (quantize) r = launch_pdl(few_rows_kernel<true, 1, 4, true>, grid, block, 0, s, p);
   else if (a.f8) r = two ? launch_pdl(few_rows_kernel<true, 2, 2, false>, grid, block, 0, s, p)
-                         : launch_pdl(few_rows_kernel<true, 1, 4, false>, grid, block, 0, s, p);
+                         : launch_pdl(few_rows_kernel<true, 1, 1, false>, grid, block, 0, s, p);
   else r = two ? launch_pdl(few_rows_kernel<false, 2, 2, false>, grid, block, 0, s, p)
                : launch_pdl(few_rows_kernel<false, 1, 4, false>, grid, block, 0, s, p);
   return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);

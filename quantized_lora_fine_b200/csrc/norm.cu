@@ -183,22 +183,27 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(NormBwd a) {
   }
 }
 
-// dw[c] = the partial rows' sum: 32 columns x 8 row groups per CTA, groups added in order.
-__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* __restrict__ part, int rows, int H,
-                                                          float* __restrict__ dw) {
-  __shared__ float s[8][33];
+// dw[c] = the partial rows' sum: 32 columns x 32 row groups per CTA, groups added in order.
+__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restrict__ part, int rows, int H,
+                                                           float* __restrict__ dw) {
+  __shared__ float s[32][33];
   pdl_wait();
   pdl_launch();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < H)
-    for (int r = g; r < rows; r += 8) v += part[int64_t(r) * H + c];
-  s[g][threadIdx.x & 31] = v;
-  __syncthreads();
-  if (g == 0 && c < H) {
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x & 31];
-    dw[c] = v;
+  if (c < H) {
+#pragma unroll 8
+    for (int r = g; r < rows; r += 32) v += part[int64_t(r) * H + c];
   }
+  s[g][lane] = v;
+  __syncthreads();
+  // warp g adds column g's groups: a fixed tree
+  v = s[lane][g];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  const int col = blockIdx.x * 32 + g;
+  if (lane == 0 && col < H) dw[col] = v;
 }
 
 struct NormShape {
@@ -243,7 +248,7 @@ cudaError_t bwd_of(const NormBwd& a, cudaStream_t s) {
 // CTAs of the backward (fixed, so that dw does not depend on the device).
 int norm_bwd_parts(int64_t M, int64_t H) {
   const int threads = norm_shape(H).threads;
-  const int per_sm = std::max(1, std::min(4, 1024 / threads));
+  const int per_sm = std::max(1, std::min(16, 1024 / threads));
   return int(std::min<int64_t>(M, int64_t(148) * per_sm));
 }
 
@@ -255,7 +260,7 @@ qlora_status launch_rms_norm_fwd(const NormFwd& a, cudaStream_t s) {
 qlora_status launch_rms_norm_bwd(const NormBwd& a, cudaStream_t s) {
   cudaError_t r = a.w_f32 ? bwd_of<true>(a, s) : bwd_of<false>(a, s);
   if (r == cudaSuccess && a.dw)
-    r = launch_pdl(rms_norm_dw_kernel, dim3(unsigned((a.H + 31) / 32)), dim3(256), 0, s, (const float*)a.part,
+    r = launch_pdl(rms_norm_dw_kernel, dim3(unsigned((a.H + 31) / 32)), dim3(1024), 0, s, (const float*)a.part,
                    norm_bwd_parts(a.M, a.H), int(a.H), a.dw);
   return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);
 }

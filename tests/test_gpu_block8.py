@@ -94,23 +94,36 @@ def _weight(o, i, seed, dev):
 SHAPES = [(16, 16), (128, 256), (272, 144), (528, 1040), (1024, 2048)]
 
 
-@pytest.mark.parametrize("o,i", SHAPES)
-@pytest.mark.parametrize("M", [1, 2, 8, 9, 16, 17, 33, 64, 77, 128, 129, 300])
-def test_linear_fwd_bwd(cuda_device, M, o, i):
-    w, W = _weight(o, i, o + i, cuda_device)
-    x, dy = outliers((M, i), M).to(cuda_device), normal((M, o), M + 1).to(cuda_device)
+def _linear(dev, M, o, i, both=True):
+    w, W = _weight(o, i, o + i, dev)
+    x, dy = outliers((M, i), M).to(dev), normal((M, o), M + 1).to(dev)
     xq, dq = api.fp8_quantize_rows(x), api.fp8_quantize_rows(dy)
     X = blocks.row_values(f64(xq.codes), f64(xq.scale).astype(np.float32))
     dY = blocks.row_values(f64(dq.codes), f64(dq.scale).astype(np.float32))
-    assert_product(f64(api.fp8_linear_fwd(w, xq)), X, W.T, "Y")
-    assert torch.equal(api.fp8_linear_fwd(w, x), api.fp8_linear_fwd(w, xq))
-    assert_product(f64(api.fp8_linear_bwd(w, dq)), dY, W, "dX")
-    assert torch.equal(api.fp8_linear_bwd(w, dy), api.fp8_linear_bwd(w, dq))
+    Y, dX = api.fp8_linear_fwd(w, xq), api.fp8_linear_bwd(w, dq)
+    assert_product(f64(Y), X, W.T, "Y")
+    assert_product(f64(dX), dY, W, "dX")
+    if both:      # bf16 rows are quantized to the same codes, with the same sums
+        assert torch.equal(api.fp8_linear_fwd(w, x), Y)
+        assert torch.equal(api.fp8_linear_bwd(w, dy), dX)
+
+
+@pytest.mark.parametrize("o,i", SHAPES)
+@pytest.mark.parametrize("M", [1, 2, 8, 9, 16, 17, 33, 64, 77, 128, 129, 300])
+def test_linear_fwd_bwd(cuda_device, M, o, i):
+    _linear(cuda_device, M, o, i)
 
 
 @pytest.mark.parametrize("M,o,i", [(700, 1024, 784), (1111, 528, 4096), (2048, 2064, 512)])
 def test_linear_larger(cuda_device, M, o, i):
-    test_linear_fwd_bwd(cuda_device, M, o, i)
+    _linear(cuda_device, M, o, i)
+
+
+@pytest.mark.parametrize("tile", ["128", "256", "pair"])
+@pytest.mark.parametrize("M,o,i", [(1, 16, 16), (9, 272, 144), (129, 528, 1040), (300, 1024, 2048), (2048, 2064, 512)])
+def test_linear_every_tile(cuda_device, monkeypatch, tile, M, o, i):
+    monkeypatch.setenv("QLORA_B200_EXPERT_TILE", tile)
+    _linear(cuda_device, M, o, i, both=False)
 
 
 @pytest.mark.parametrize("M", [5, 300])

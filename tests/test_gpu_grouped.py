@@ -72,6 +72,22 @@ def test_grouped(cuda_device, groups, o, i, kind):
     _run(cuda_device, GROUPS[groups], o, i, kind)
 
 
+@pytest.mark.parametrize("tile", ["128", "256", "pair"])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("o,i", [(144, 272), (528, 1024)])
+@pytest.mark.parametrize("groups", list(GROUPS))
+def test_grouped_every_tile(cuda_device, monkeypatch, tile, groups, o, i, kind):
+    monkeypatch.setenv("QLORA_B200_EXPERT_TILE", tile)
+    _run(cuda_device, GROUPS[groups], o, i, kind, before=1, after=30)
+
+
+@pytest.mark.parametrize("sizes", [[1], [2, 1, 0, 3, 1, 1, 0, 1], [0, 0, 0, 9]])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_few_rows_a_group(cuda_device, sizes, kind):
+    """The decoding kernel, with more rows in one group than it takes in a pass."""
+    _run(cuda_device, sizes, 272, 1360, kind, before=0, after=0)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("groups", ["with empty", "step edges", "large"])
 def test_rows_outside_groups(cuda_device, groups, kind):

@@ -137,3 +137,11 @@ def test_binding_refuses_cpu_tensors():
                  lambda: api.grouped_linear_fwd(x.view(1, 4, 64), x, off)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_status_word_is_not_set_up_while_capturing(monkeypatch):
+    """The first call on a device allocates the status word; under capture that is refused in words."""
+    monkeypatch.setattr(api.Workspace, "_bufs", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="before capturing"):
+        api.Workspace.status_word(0)

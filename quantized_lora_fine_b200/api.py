@@ -455,10 +455,10 @@ def _check_weight_vector(w: torch.Tensor, H: int, device: int) -> int:
     return DTYPE_F32
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class FP8Rows:
     """Rows in e4m3: codes float8_e4m3fn [M, in], scale fp32 [M, ceil(in / 128)]; a value
-    is its code times its block's scale."""
+    is its code times its block's scale. Checked once, when made."""
     codes: torch.Tensor
     scale: torch.Tensor
 
@@ -468,11 +468,11 @@ class FP8Rows:
         _check(self.scale, _F32, (M, _blocks(n)), "scale", self.codes.get_device())
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class FP8Weight:
     """A frozen weight in e4m3, stored out x in: codes float8_e4m3fn [out, in], or
     [experts, out, in], with a scale for each 128 x 128 block, fp32
-    [(experts,) ceil(out / 128), ceil(in / 128)]."""
+    [(experts,) ceil(out / 128), ceil(in / 128)]. Checked once, when made."""
     codes: torch.Tensor
     scale: torch.Tensor
 
@@ -495,24 +495,32 @@ class FP8Weight:
 
 def _new_rows(M: int, n: int, device) -> FP8Rows:
     r = object.__new__(FP8Rows)
-    r.codes = torch.empty((M, n), dtype=_F8, device=device)
-    r.scale = torch.empty((M, _blocks(n)), dtype=_F32, device=device)
+    r.__dict__.update(codes=torch.empty(M, n, dtype=_F8, device=device),
+                      scale=torch.empty(M, _blocks(n), dtype=_F32, device=device))
     return r
+
+
+def _status_ptr(device: int) -> int:
+    buf = Workspace._bufs.get((device, None))
+    return (Workspace.status_word(device) if buf is None else buf).data_ptr()
 
 
 def _expert_weight(W, device: int) -> Tuple[_lib.ExpertWeight, int, int, int]:
     """(descriptor, experts, out, in) of an FP8Weight or a bf16 tensor [(experts,) out, in]."""
-    t = W.codes if isinstance(W, FP8Weight) else W
-    shape = t.shape
-    E = shape[0] if len(shape) == 3 else 1
-    if t is not W:
-        _check(t, _F8, shape, "W.codes", device)
-        _check(W.scale, _F32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), "W.scale", device)
-        return _lib.ExpertWeight(E, shape[-2], shape[-1], 0, t.data_ptr(), W.scale.data_ptr(), None), E, *shape[-2:]
+    if isinstance(W, FP8Weight):
+        t = W.codes
+        if t.get_device() != device:
+            raise ValueError(f"every tensor of a call must be on one device: the weight is on {t.device}, "
+                             f"not cuda:{device}")
+        shape = t.shape
+        E, o, i = shape if len(shape) == 3 else (1, *shape)
+        return _lib.ExpertWeight(E, o, i, 0, t.data_ptr(), W.scale.data_ptr(), None), E, o, i
+    t, shape = W, W.shape
     if len(shape) not in (2, 3):
         raise ValueError("W must be [out, in] or [experts, out, in]")
     _check(t, _BF16, shape, "W", device)
-    return _lib.ExpertWeight(E, shape[-2], shape[-1], 1, None, None, t.data_ptr()), E, *shape[-2:]
+    E, o, i = shape if len(shape) == 3 else (1, *shape)
+    return _lib.ExpertWeight(E, o, i, 1, None, None, t.data_ptr()), E, o, i
 
 
 def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -617,8 +625,6 @@ def _rows_of(rows, eight_bit: bool, cols: int, name: str):
             raise ValueError(f"{name}: FP8Rows need an FP8Weight")
         t, sc = rows.codes, rows.scale
         dev = t.get_device()
-        _check(t, _F8, None, name)
-        _check(sc, _F32, (t.shape[0], _blocks(t.shape[1])), name + ".scale", dev)
     else:
         _check(rows, _BF16, None, name)
         t, sc, dev = rows, None, rows.get_device()
@@ -629,7 +635,7 @@ def _rows_of(rows, eight_bit: bool, cols: int, name: str):
 
 def _output(t: Optional[torch.Tensor], shape: tuple, dtype, like: torch.Tensor, dev: int, name: str) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(*shape, dtype=dtype, device=like.device)
     _check(t, dtype, shape, name, dev)
     return t
 
@@ -649,15 +655,15 @@ def fp8_linear_fwd(w: FP8Weight, X, Y: Optional[torch.Tensor] = None) -> torch.T
     if sx is None and M > _FP8_BF16_ROWS:
         q = fp8_quantize_rows(x)
         x, sx = q.codes, q.scale
-    ws = Workspace.status_word(dev)
+    ws = _status_ptr(dev)
     Y = _output(Y, (M, w.out), _BF16, x, dev, "Y")
-    check(lib.fp8_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), M, Y.data_ptr(), ws.data_ptr(), 256,
+    check(lib.fp8_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), M, Y.data_ptr(), ws, 256,
                              _raw_stream(dev)), "fp8_linear_fwd")
     return Y
 
 
 # Rows up to which fp8_linear_fwd takes bf16 and quantizes within its kernel (fp8_linear_bf16_rows()).
-_FP8_BF16_ROWS = 8
+_FP8_BF16_ROWS = 2
 
 
 def fp8_linear_bwd(w: FP8Weight, dY, dX: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -673,10 +679,10 @@ def fp8_linear_bwd(w: FP8Weight, dY, dX: Optional[torch.Tensor] = None) -> torch
     if sd is None:
         q = fp8_quantize_rows(d)
         d, sd = q.codes, q.scale
-    ws = Workspace.status_word(dev)
+    ws = _status_ptr(dev)
     dX = _output(dX, (d.shape[0], w.inp), _BF16, d, dev, "dX")
     check(_lib.load().fp8_linear_bwd(ctypes.byref(cs), d.data_ptr(), sd.data_ptr(), d.shape[0], dX.data_ptr(),
-                                     ws.data_ptr(), 256, _raw_stream(dev)), "fp8_linear_bwd")
+                                     ws, 256, _raw_stream(dev)), "fp8_linear_bwd")
     return dX
 
 
@@ -695,10 +701,10 @@ def grouped_linear_fwd(W, X, offsets: torch.Tensor, Y: Optional[torch.Tensor] = 
     if eight and sx is None:
         q = fp8_quantize_rows(x)
         x, sx = q.codes, q.scale
-    ws = Workspace.status_word(dev)
+    ws = _status_ptr(dev)
     Y = _output(Y, (x.shape[0], o), _BF16, x, dev, "Y")
     check(_lib.load().qlora_grouped_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), x.shape[0],
-                                               offsets.data_ptr(), Y.data_ptr(), ws.data_ptr(), 256,
+                                               offsets.data_ptr(), Y.data_ptr(), ws, 256,
                                                _raw_stream(dev)), "qlora_grouped_linear_fwd")
     return Y
 
@@ -729,11 +735,11 @@ def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, 
     if eight and sd is None:
         q = fp8_quantize_rows(d)
         d, sd = q.codes, q.scale
-    ws = Workspace.status_word(dev)
+    ws = _status_ptr(dev)
     dX = _output(dX, (M, i), _BF16, d, dev, "dX") if need_dX else None
     dW = _output(dW, (E, o, i), _F32, d, dev, "dW") if need_dW else None
     check(_lib.load().qlora_grouped_linear_bwd(ctypes.byref(cs), xp, d.data_ptr(), _ptr(sd), M, offsets.data_ptr(),
-                                               _ptr(dX), _ptr(dW), ws.data_ptr(), 256, _raw_stream(dev)),
+                                               _ptr(dX), _ptr(dW), ws, 256, _raw_stream(dev)),
           "qlora_grouped_linear_bwd")
     return dX, dW
 

@@ -35,7 +35,7 @@ qlora_status launch_expert_gemm(const ExpertArgs& a, cudaStream_t s);
 
 // few_rows.cu: Fwd with few rows a group. With `quantize` the rows are bf16 (at most
 // kFewQuantRows in all, one group) and the weight e4m3.
-constexpr int64_t kFewQuantRows = 8;
+constexpr int64_t kFewQuantRows = 2;
 bool few_rows_wanted(const ExpertArgs& a);
 qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s);
 

@@ -2,15 +2,19 @@
 //
 // A CTA takes 16 rows of one expert's weight over all of K, its 8 warps every eighth
 // 128-byte block of K. The rows stream from global memory into the registers of
-// mma.sync fragments: lane (g, t) loads 32 neighbouring bytes of weight rows g and
-// g + 8, and the same 32 bytes of token g, and gives their words to four products in
-// the same order on both sides (a sum over k may run over k in any order), so every load
-// is 16 bytes wide and nothing passes through shared memory. Weight rows are the
-// product's 16 rows, tokens its 8 columns. In e4m3 a block's product is scaled by sa sb
-// and added in fp32; the warps' sums are added in order at the end.
+// mma.sync fragments: lane (g, t) loads bytes 16 t .. and 64 + 16 t .. of weight rows g and
+// g + 8 and of token g, and gives their words to four products in the same order on both
+// sides (a sum over k may run over k in any order), so every load is 16 bytes wide, a warp's
+// cover whole sectors and nothing passes through shared memory. Weight rows are the
+// product's 16 rows, tokens its 8 columns. In e4m3 a block's product is scaled by sa sb and
+// added in fp32; the warps' sums are added in order at the end. 32 experts of 2048 x 4096, 31
+// of them with rows, 4 on average: bf16 84 us, 95 % of the copy bandwidth; e4m3, whose
+// products the hardware takes through 16-bit ones, 51 us, 77 %. (Weights by cp.async into
+// shared memory, 4 blocks ahead: 64 us.)
 //
-// With bf16 rows and an e4m3 weight (QUANT, up to 8 rows in all) each warp quantizes the
-// blocks that it multiplies, as quantize_rows8_kernel does, which saves that launch.
+// With bf16 rows and an e4m3 weight (QUANT, up to 2 rows in all) each warp quantizes the
+// blocks that it multiplies, as quantize_rows8_kernel does, which saves that launch (every
+// CTA quantizes every row: at 8 rows that took longer than the launch).
 //
 // tcgen05 tiles of 128 rows would leave most SMs without a tile here: 4096 x 4096 has 32.
 #include <algorithm>
@@ -58,11 +62,11 @@ __device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1,
   }
 }
 
-// 32 bytes at p; zero where the row ends (at a multiple of 16).
+// 16 bytes at p and 16 at p + 64; zero where the row ends (at a multiple of 16; `left` from p).
 __device__ __forceinline__ void load32(uint32_t (&v)[8], const uint8_t* p, int left) {
   const uint4 z = make_uint4(0, 0, 0, 0);
   const uint4 a = left >= 16 ? __ldg(reinterpret_cast<const uint4*>(p)) : z;
-  const uint4 b = left >= 32 ? __ldg(reinterpret_cast<const uint4*>(p) + 1) : z;
+  const uint4 b = left >= 80 ? __ldg(reinterpret_cast<const uint4*>(p) + 4) : z;
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -70,18 +74,18 @@ __device__ __forceinline__ void load32(uint32_t (&v)[8], const uint8_t* p, int l
 __device__ __forceinline__ void stream32(uint32_t (&v)[8], const uint8_t* p, int left) {
   const uint4 z = make_uint4(0, 0, 0, 0);
   const uint4 a = left >= 16 ? __ldcs(reinterpret_cast<const uint4*>(p)) : z;
-  const uint4 b = left >= 32 ? __ldcs(reinterpret_cast<const uint4*>(p) + 1) : z;
+  const uint4 b = left >= 80 ? __ldcs(reinterpret_cast<const uint4*>(p) + 4) : z;
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 // NT: 8-token columns a pass; U: blocks of K in flight a warp.
 template <bool F8, int NT, int U, bool QUANT>
-__global__ void __launch_bounds__(kFewWarps * 32, (F8 && !QUANT && NT == 1) ? 4 : 2) few_rows_kernel(const FewParams p) {
-  static_assert(!QUANT || (F8 && NT == 1), "rows quantized here are at most 8, in e4m3");
+__global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_rows_kernel(const FewParams p) {
+  static_assert(kFewQuantRows == 2, "tokens 0 and 1 are lane t = 0's");
+  static_assert(!QUANT || (F8 && NT == 1 && U == 1), "rows quantized here: kFewQuantRows, in e4m3");
   __shared__ float red[kFewWarps][NT * 8][17];
-  __shared__ __align__(16) uint8_t xq[QUANT ? kFewWarps * U * 8 * 128 : 16];
-  __shared__ float xs[QUANT ? kFewWarps * U * 8 : 1];
+  __shared__ __align__(16) uint8_t xq[QUANT ? kFewWarps * kFewQuantRows * 128 : 16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int e = blockIdx.y, n0 = blockIdx.x * 16;
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, (F8 && !QUANT && NT == 1) ? 4 
     if (blockIdx.x == 0 && threadIdx.x == 0 && (r0 < 0 || r1 > p.M || r1 < r0))
       set_status_site(p.status, QLORA_ERR_SHAPE, 70);
   }
-  const uint8_t* w0 = p.w + (int64_t(e) * p.out + n0 + g) * p.wbytes + 32 * t;
+  const uint8_t* w0 = p.w + (int64_t(e) * p.out + n0 + g) * p.wbytes + 16 * t;
   const uint8_t* w1 = w0 + int64_t(8) * p.wbytes;
   const float* sb = F8 ? p.sb + (int64_t(e) * p.nb_n + (n0 >> 7)) * p.nk : nullptr;
 
@@ -110,62 +114,69 @@ __global__ void __launch_bounds__(kFewWarps * 32, (F8 && !QUANT && NT == 1) ? 4 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    uint2 xv[kFewQuantRows];                       // QUANT: the next block of every row, 4 values a lane
+    auto fetch = [&](int k) {
+      const int col = k * 128 + lane * 4;
+#pragma unroll
+      for (int m = 0; m < kFewQuantRows; ++m)
+        xv[m] = (m0 + m < last && col < p.in)
+                    ? __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.x) +
+                                                           int64_t(m0 + m) * p.in + col))
+                    : make_uint2(0, 0);
+    };
+    if constexpr (QUANT) fetch(warp);
     for (int k0 = warp; k0 < p.nk; k0 += kFewWarps * U) {
       uint32_t a[U][2][8], b[U][NT][8];
       float f[U][NT][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * kFewWarps;
-        const int left = k < p.nk ? p.wbytes - k * 128 - 32 * t : 0;
+        const int left = k < p.nk ? p.wbytes - k * 128 - 16 * t : 0;
         stream32(a[u][0], w0 + int64_t(k) * 128, left);
         stream32(a[u][1], w1 + int64_t(k) * 128, left);
       }
+      float xs[2] = {0.f, 0.f};                    // QUANT: scales of tokens 2 t, 2 t + 1
       if constexpr (QUANT) {
-        uint8_t* xw = xq + warp * U * 8 * 128;
-        float* sw = xs + warp * U * 8;
+        // this block of every row to codes in the warp's own shared memory
+        uint8_t* xw = xq + warp * kFewQuantRows * 128;
+        uint2 v[kFewQuantRows];
+#pragma unroll
+        for (int m = 0; m < kFewQuantRows; ++m) v[m] = xv[m];
+        fetch(k0 + kFewWarps);
         __syncwarp();
-        for (int m = 0; m < last - m0; ++m) {      // at most 8 rows
-          uint2 v[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int col = (k0 + u * kFewWarps) * 128 + lane * 4;
-            v[u] = col < p.in ? __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.x) +
-                                                                     int64_t(m0 + m) * p.in + col))
-                              : make_uint2(0, 0);
-          }
+        for (int m = 0; m < kFewQuantRows; ++m) {
+          uint32_t mx = max(max(v[m].x & 0x7FFFu, (v[m].x >> 16) & 0x7FFFu),
+                            max(v[m].y & 0x7FFFu, (v[m].y >> 16) & 0x7FFFu)) << 16;
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const float q0 = __uint_as_float(v[u].x << 16), q1 = __uint_as_float(v[u].x & 0xFFFF0000u);
-            const float q2 = __uint_as_float(v[u].y << 16), q3 = __uint_as_float(v[u].y & 0xFFFF0000u);
-            uint32_t mx = max(max(v[u].x & 0x7FFFu, (v[u].x >> 16) & 0x7FFFu),
-                              max(v[u].y & 0x7FFFu, (v[u].y >> 16) & 0x7FFFu)) << 16;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const Block8 q = block8_of(mx);
-            reinterpret_cast<uint32_t*>(xw + (u * 8 + m) * 128)[lane] =
-                e4m3x4(block8_quotient(q0, q), block8_quotient(q1, q), block8_quotient(q2, q), block8_quotient(q3, q));
-            if (lane == 0) sw[u * 8 + m] = q.scale;
-          }
+          for (int d = 16; d > 0; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          const Block8 q = block8_of(mx);
+          reinterpret_cast<uint32_t*>(xw + m * 128)[lane] =
+              e4m3x4(block8_quotient(__uint_as_float(v[m].x << 16), q),
+                     block8_quotient(__uint_as_float(v[m].x & 0xFFFF0000u), q),
+                     block8_quotient(__uint_as_float(v[m].y << 16), q),
+                     block8_quotient(__uint_as_float(v[m].y & 0xFFFF0000u), q));
+          if (t == 0) xs[m] = q.scale;
         }
         __syncwarp();
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * kFewWarps;
-        const int left = k < p.nk ? p.wbytes - k * 128 - 32 * t : 0;
+        const int left = k < p.nk ? p.wbytes - k * 128 - 16 * t : 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int m = m0 + n * 8 + g;
           if constexpr (QUANT) {
-            const uint8_t* src = xq + ((warp * U + u) * 8 + g) * 128 + 32 * t;
-            const bool live = m < last && k < p.nk;
+            const uint8_t* src = xq + (warp * kFewQuantRows + (g & 1)) * 128 + 16 * t;
+            const bool live = g < kFewQuantRows && m < last;
             const uint4 z = make_uint4(0, 0, 0, 0);
             const uint4 lo = live ? reinterpret_cast<const uint4*>(src)[0] : z;
-            const uint4 hi = live ? reinterpret_cast<const uint4*>(src)[1] : z;
+            const uint4 hi = live ? reinterpret_cast<const uint4*>(src)[4] : z;
             b[u][n][0] = lo.x; b[u][n][1] = lo.y; b[u][n][2] = lo.z; b[u][n][3] = lo.w;
             b[u][n][4] = hi.x; b[u][n][5] = hi.y; b[u][n][6] = hi.z; b[u][n][7] = hi.w;
           } else {
-            load32(b[u][n], p.x + int64_t(m) * p.wbytes + k * 128 + 32 * t, m < last ? left : 0);
+            load32(b[u][n], p.x + int64_t(m) * p.wbytes + k * 128 + 16 * t, m < last ? left : 0);
           }
           if constexpr (F8) {
 #pragma unroll
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, (F8 && !QUANT && NT == 1) ? 4 
               const int c = m0 + n * 8 + 2 * t + h;
               f[u][n][h] = 0.f;
               if (c < last && k < p.nk) {
-                if constexpr (QUANT) f[u][n][h] = xs[(warp * U + u) * 8 + 2 * t + h] * __ldg(sb + k);
+                if constexpr (QUANT) f[u][n][h] = xs[h] * __ldg(sb + k);
                 else f[u][n][h] = __ldg(p.sa + int64_t(c) * p.nk + k) * __ldg(sb + k);
               }
             }
@@ -219,13 +230,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, (F8 && !QUANT && NT == 1) ? 4 
 
 }  // namespace
 
-// Up to 16 rows of one group, or 2 a group on average (more rows are right, pass by pass,
+// Up to 16 rows of one group, or 4 a group on average (more rows are right, pass by pass,
 // but each pass fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 6.7 us against 16.6
-// with tiles; 64 experts of 1024 x 2048 in bf16: 32 us against 37 at one row a group, 47.5
-// against 49 at four, 80 against 50 at sixteen. QLORA_B200_EXPERT_TILE set: never.
+// with tiles; 64 experts of 1024 x 2048 in bf16: 32 us against 43 at one row a group, 48
+// against 48 at four, 80 against 50 at sixteen; in e4m3 18 against 25, and 32 against 30.
+// QLORA_B200_EXPERT_TILE set: never.
 bool few_rows_wanted(const ExpertArgs& a) {
   if (a.mode != ExpertMode::Fwd || std::getenv("QLORA_B200_EXPERT_TILE")) return false;
-  return a.offsets ? a.M <= 2 * a.E : a.M <= 16;
+  return a.offsets ? a.M <= 4 * a.E : a.M <= 16;
 }
 
 qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s) {
@@ -247,7 +259,7 @@ qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s)
   const dim3 grid(unsigned(a.out / 16), unsigned(a.E)), block(kFewWarps * 32);
   const bool two = !quantize && !a.offsets && a.M > 8;
   cudaError_t r;
-  if (quantize) r = launch_pdl(few_rows_kernel<true, 1, 4, true>, grid, block, 0, s, p);
+  if (quantize) r = launch_pdl(few_rows_kernel<true, 1, 1, true>, grid, block, 0, s, p);
   else if (a.f8) r = two ? launch_pdl(few_rows_kernel<true, 2, 2, false>, grid, block, 0, s, p)
                          : launch_pdl(few_rows_kernel<true, 1, 1, false>, grid, block, 0, s, p);
   else r = two ? launch_pdl(few_rows_kernel<false, 2, 2, false>, grid, block, 0, s, p)

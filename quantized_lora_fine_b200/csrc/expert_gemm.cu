@@ -97,7 +97,8 @@ struct ExpertCfg {
   static constexpr int kThreads = (4 + kEpiWarps) * 32;
   static constexpr int kRoleRegs = 56, kEpiRegs = 224;  // WIDE
   static_assert(!WIDE || (kThreads == 384 && kRoleRegs * 128 + kEpiRegs * 256 <= 168 * 384), "register split");
-  static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kBufs = F8 ? 512 / BN : 2;       // TMEM buffers of BN columns
+  static constexpr int kTmemCols = kBufs * BN;
   static constexpr int kPassCols = DW ? 32 : 64;        // D columns in 128 bytes
   static constexpr int kStgBufs = 1;               // staging buffers per epilogue warp
   static constexpr int kStaging = kEpiWarps * kStgBufs * 4096;   // 32 rows x 128 bytes each
@@ -106,7 +107,7 @@ struct ExpertCfg {
   static constexpr int kScaleSlot = 4 * kBlocksN * 512; // 4 steps x column blocks x 128 rows
   static constexpr int kScaleOff = STAGES * kStage + kStaging;
   static constexpr int kBarOff = kScaleOff + (F8 ? kScaleSlots * kScaleSlot : 0);
-  static constexpr int kNumBars = 3 * STAGES + 5 + 2 * kScaleSlots;
+  static constexpr int kNumBars = 3 * STAGES + 2 * kBufs + 1 + 2 * kScaleSlots;
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kSmem = kTableOff + 2 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -184,11 +185,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
   auto tfull_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
-  auto tempty_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
-  auto tail_bar = [&](int i) { return bars + 8u * (2 * C::STAGES + 4 + i); };
-  const uint32_t drain_bar = bars + 8u * (3 * C::STAGES + 4);
-  auto sfull_bar = [&](int s) { return bars + 8u * (3 * C::STAGES + 5 + s); };
-  auto sempty_bar = [&](int s) { return bars + 8u * (3 * C::STAGES + 5 + C::kScaleSlots + s); };
+  auto tempty_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + C::kBufs + b); };
+  constexpr int kB0 = 2 * C::STAGES + 2 * C::kBufs;
+  auto tail_bar = [&](int i) { return bars + 8u * (kB0 + i); };
+  auto sfull_bar = [&](int s) { return bars + 8u * (kB0 + C::STAGES + s); };
+  auto sempty_bar = [&](int s) { return bars + 8u * (kB0 + C::STAGES + C::kScaleSlots + s); };
+  const uint32_t drain_bar = bars + 8u * (kB0 + C::STAGES + 2 * C::kScaleSlots);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kNumBars);
   int* starts = reinterpret_cast<int*>(smem + C::kTableOff);
   int* tiles = starts + kMaxExperts + 1;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(full_bar(s), C::PAIR ? 2 : 1);   // one arrival per CTA's producer
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), (C::PAIR ? 2 : 1) * C::kEpiWarps);
     }
@@ -283,35 +285,32 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if constexpr (C::WIDE) regs_down<C::kRoleRegs>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&tmA);
       tma_prefetch_desc(&tmB);
-    }
-    uint32_t it = 0, ntail = 0;
-    int e = 0;
-    bool ok = true;
-    for (int t = unit; t < num_tiles && ok; t += units) {
-      const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
-      const int a_rows = min(128, max(0, x.rows - int(rank) * 128));
-      const int boxes = C::A_MN || C::PAIR ? 1 : (a_rows + p.a_box - 1) / p.a_box;
-      const int b0 = x.n0 + int(rank) * C::BCTA;    // this CTA's columns of B
-      const int a0 = x.row0 + int(rank) * 128;      // this CTA's rows of D
-      for (int kb = 0; kb < x.nk; ++kb, ++it) {
-        const int s = it % C::STAGES;
-        const uint32_t ph = (it / C::STAGES) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait_lazy(empty_bar(s), ph ^ 1u))) {
-          if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 61);
-          ok = false;
-          break;
-        }
-        const uint32_t a_s = base + s * C::kStage, b_s = a_s + C::kA;
-        const int valid = C::DW ? x.k_rows - kb * C::BK : C::BK;   // rows of the reduction in this step
-        const bool tail = C::DW && valid < C::BK;
-        if (lane == 0) {
+      uint32_t s = 0, ph = 1, ntail = 0;   // stage, and the parity that says it is free
+      uint32_t issued = 0;
+      int e = 0;
+      bool ok = true;
+      for (int t = unit; t < num_tiles && ok; t += units) {
+        const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
+        const int a_rows = min(128, max(0, x.rows - int(rank) * 128));
+        const int boxes = C::A_MN || C::PAIR ? 1 : (a_rows + p.a_box - 1) / p.a_box;
+        const int b0 = x.n0 + int(rank) * C::BCTA;    // this CTA's columns of B
+        const int a0 = x.row0 + int(rank) * 128;      // this CTA's rows of D
+        for (int kb = 0; kb < x.nk; ++kb) {
+          if (!mbar_wait_lazy(empty_bar(s), ph)) {
+            set_status_site(p.status, QLORA_ERR_TIMEOUT, 61);
+            ok = false;
+            break;
+          }
+          const uint32_t a_s = base + s * C::kStage, b_s = a_s + C::kA;
+          const bool tail = C::DW && x.k_rows - kb * C::BK < C::BK;
           uint32_t bar;
           if (tail) {
             // landed on a barrier of its own, which warp 2 waits on; it hands the stage over
             bar = tail_bar(ntail % C::STAGES);
+            ++ntail;
             mbar_arrive_expect_tx(bar, C::kStage);
           } else if constexpr (C::PAIR) {
             // The even CTA's barrier counts both CTAs' bytes.
@@ -347,21 +346,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 load3(b_s + c * C::BK * 128, &tmB, b0 + c * C::kChunk, k0);
             }
           }
+          ++issued;
+          if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
-        if (tail) ++ntail;
-        __syncwarp();
+      }
+      // Do not leave while copies may still be landing (after an error; else all are consumed).
+      if (!ok && rank == 0) {
+        for (uint32_t k = 0; k < uint32_t(C::STAGES) && k < issued; ++k) {
+          const uint32_t i2 = issued - 1 - k;
+          mbar_wait(full_bar(i2 % C::STAGES), (i2 / C::STAGES) & 1u, kDrainNs);
+        }
       }
     }
-    // Do not leave while copies may still be landing (after an error; else all are consumed).
-    if (!ok && it > 0 && rank == 0) {
-      for (uint32_t k = 0; k < uint32_t(C::STAGES) && k < it; ++k) {
-        const uint32_t i2 = it - 1 - k;
-        mbar_wait_lazy(full_bar(i2 % C::STAGES), (i2 / C::STAGES) & 1u, kDrainNs);
-      }
-    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = C::F8 ? make_idesc_e4m3(C::BM, C::BN, C::A_MN, C::B_MN)
                                        : make_idesc_bf16(C::BM, C::BN, C::A_MN, C::B_MN);
       // K advance per instruction (32 bytes of K): inside a K-major row, or that many
@@ -370,22 +370,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       constexpr uint32_t a_adv = C::A_MN ? mn_adv : 32u, b_adv = C::B_MN ? mn_adv : 32u;
       constexpr uint32_t mn_lbo = C::BK * 128u;   // bytes between MN-major column chunks
       constexpr uint32_t a_lbo = C::A_MN ? mn_lbo : 16u, b_lbo = C::B_MN ? mn_lbo : 16u;
-      uint32_t it = 0, u = 0;
+      const uint64_t ad0 = make_smem_desc(base, a_lbo, 1024u, kSwizzle128B);
+      const uint64_t bd0 = make_smem_desc(base + C::kA, b_lbo, 1024u, kSwizzle128B);
+      uint32_t s = 0, ph = 0, u = 0;
       int e = 0;
       bool ok = true;
       for (int t = unit; t < num_tiles && ok; t += units) {
         const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
-        for (int kb = 0; kb < x.nk; ++kb, ++it) {
-          const uint32_t buf = u & 1u;
+        for (int kb = 0; kb < x.nk; ++kb) {
+          const uint32_t buf = u % C::kBufs;
           if (C::F8 || kb == 0) {
-            if (!mbar_wait_lazy(tempty_bar(buf), ((u >> 1) & 1u) ^ 1u)) {
+            if (!mbar_wait_lazy(tempty_bar(buf), ((u / C::kBufs) & 1u) ^ 1u)) {
               set_status_site(p.status, QLORA_ERR_TIMEOUT, 63);
               ok = false;
               break;
             }
           }
-          const int s = it % C::STAGES;
-          const uint32_t ph = (it / C::STAGES) & 1u;
           // (cluster scope where the other CTA's generic stores, a cleared tail, are handed over)
           const bool tail = C::PAIR && C::DW && x.k_rows - kb * C::BK < C::BK;
           if (!(tail ? mbar_wait_cluster(full_bar(s), ph) : mbar_wait_lazy(full_bar(s), ph))) {
@@ -394,9 +394,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t st = base + s * C::kStage;
-          const uint64_t ad = make_smem_desc(st, a_lbo, 1024u, kSwizzle128B);
-          const uint64_t bd = make_smem_desc(st + C::kA, b_lbo, 1024u, kSwizzle128B);
+          const uint64_t ad = ad0 + uint64_t(s * (C::kStage >> 4)), bd = bd0 + uint64_t(s * (C::kStage >> 4));
           const uint32_t d = tmem + buf * C::BN;
 #pragma unroll
           for (uint32_t kk = 0; kk < 4; ++kk) {
@@ -417,6 +415,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             else tc_commit(tfull_bar(buf));
             ++u;
           }
+          if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
       }
       // All MMAs of this thread are complete once drain_bar flips.
@@ -528,8 +527,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
       // Adds s times the next TMEM buffer to acc, and hands the buffer back.
       auto take = [&](float s) {
-        const uint32_t buf = u & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait_lazy(tfull_bar(buf), (u >> 1) & 1u))) {
+        const uint32_t buf = u % C::kBufs;
+        if (!__all_sync(0xffffffffu, mbar_wait_lazy(tfull_bar(buf), (u / C::kBufs) & 1u))) {
           if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 65);
           ok = false;   // (and on, so that the sums have one path: they are not stored)
         }

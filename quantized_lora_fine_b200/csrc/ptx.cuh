@@ -215,6 +215,14 @@ __device__ __forceinline__ void st_async_signal(uint32_t dst_cluster, uint32_t b
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// True in one lane of a converged warp. (The compiler knows that the code under it runs in one
+// lane, so the operands of tensor and copy instructions can stay in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Registers per thread of this warpgroup from here on (all four warps together). The block's
 // warpgroups may hold no more than its threads x its registers at launch between them.
 template <int N>

@@ -752,16 +752,20 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
 }
 
 // The tile: by the time that the waves of tiles take, a wave's steps at the rates measured
-// with full waves (us per step of 128 bytes of K):
+// with full waves (us per step of 128 bytes of K; bf16 128 x 256 a tenth above its rate with
+// operands in L2, for the weights of groups come from HBM):
 //                  e4m3    bf16
-//   128 x 128      0.47    0.40     148 at once; the most units and the fewest wasted rows
-//   128 x 256      0.65    0.48     148 at once
-//   256 x 256 pair 0.62    0.44     74 at once; half the L2 bytes of 128 x 128 per product
-// (e4m3 4096 x 4096 at 512 rows: 18.5, 21.8 and 22.0 us; at 768: 32.1, 22.7 and 22.6; at
-// 8192: 202, 143 and 137.) The row tiles of groups, whose sizes are on the device, are taken as
-// half a tile more than full for each group. Dw, which writes fp32 and has few steps a tile,
-// by the waves alone (16 experts of 1408 x 2048, 512 rows each: 84, 79 and 82 us, waves of 20,
-// 10 and 11; 64 of 1024 x 2048, 64 rows each: 116, 112 and 98 us, 28 waves of either).
+//   128 x 128      0.40    0.27     148 at once; the most units and the fewest wasted rows
+//   128 x 256      0.64    0.52     148 at once
+//   256 x 256 pair 0.61    0.386    74 at once; half the L2 bytes of 128 x 128 per product
+// (e4m3 4096 x 4096 at 512 rows: 15.9, 21.4 and 21.4 us; at 2048: 54, 41 and 41; at 8192: 177,
+// 142 and 136. bf16 at 8192: 251, 207 and 173.) Groups' sizes are on the device: their row
+// tiles are taken as half a tile more than full for each group, and the waves, where they
+// are not safely one, as half a wave more (16 experts of 1408 x 2048 in bf16, 128 rows each
+// on average: 25, 36 and 29 us; 64 of 1024 x 2048, 256 rows each: 99, 97 and 82).
+// Dw, which writes fp32 and has few steps a tile, by the waves, a pair's a tenth shorter (16
+// experts of 1408 x 2048, 512 rows each: 79, 76 and 71 us, waves of 20, 10 and 11; 64 of 1024 x
+// 2048, 64 rows each: 116, 112 and 97 us, 28 waves of either).
 // QLORA_B200_EXPERT_TILE=128|256|pair overrides the choice, for measurement and tests.
 enum class ExpertTileKind { T128, T256, Pair };
 template <bool F8>
@@ -777,17 +781,18 @@ ExpertTileKind tile_kind(const ExpertArgs& a) {
     auto waves = [&](int bm, int at_once) {
       return (a.E * ((a.out + bm - 1) / bm) * ((a.in + 255) / 256) + at_once - 1) / at_once;
     };
-    return waves(256, 74) <= waves(128, 148) ? ExpertTileKind::Pair : ExpertTileKind::T256;
+    return 9 * waves(256, 74) <= 10 * waves(128, 148) ? ExpertTileKind::Pair : ExpertTileKind::T256;
   }
   const int64_t N = a.mode == ExpertMode::Fwd ? a.out : a.in;
   auto cost = [&](int bm, int bn, int at_once, double step) {
-    int64_t rt = (a.M + bm - 1) / bm;
-    if (a.offsets) rt = std::max(std::min(a.E, a.M), a.M / bm + a.E / 2);
-    const int64_t tiles = rt * ((N + bn - 1) / bn);
-    return double((tiles + at_once - 1) / at_once) * step;
+    const int64_t cols = (N + bn - 1) / bn;
+    if (!a.offsets) return double(((a.M + bm - 1) / bm * cols + at_once - 1) / at_once) * step;
+    const double rows = std::max(double(std::min(a.E, a.M)), double(a.M) / bm + 0.5 * double(a.E));
+    const double waves = rows * double(cols) / at_once;
+    return (waves <= 0.9 ? 1.0 : waves + 0.5) * step;
   };
-  const double c128 = cost(128, 128, 148, F8 ? 0.47 : 0.40), c256 = cost(128, 256, 148, F8 ? 0.65 : 0.48),
-               cpair = cost(256, 256, 74, F8 ? 0.62 : 0.44);
+  const double c128 = cost(128, 128, 148, F8 ? 0.40 : 0.27), c256 = cost(128, 256, 148, F8 ? 0.64 : 0.52),
+               cpair = cost(256, 256, 74, F8 ? 0.61 : 0.386);
   if (cpair <= c256 && cpair <= c128) return ExpertTileKind::Pair;
   return c256 <= c128 ? ExpertTileKind::T256 : ExpertTileKind::T128;
 }

@@ -12,7 +12,8 @@
 // The inner sums run on the tensor cores, 128 values deep, into a fresh TMEM buffer
 // for each k; the outer sum is one fp32 multiply-add per value in the registers of
 // the epilogue warps, which read buffer k while the tensor cores fill buffer k + 1.
-// In bf16 the tensor cores sum over all of K and the epilogue reads once per tile.
+// In bf16 the tensor cores sum over all of K and the epilogue reads once per tile (Dw, which
+// stays in fp32: every 256 rows).
 //
 // One persistent CTA per SM, or one CTA pair per two SMs (cta_group::2, tiles of 256 x
 // 256: each CTA stages its 128 rows of A and its 128 columns of B, so a byte from L2
@@ -97,6 +98,13 @@ struct ExpertCfg {
   static constexpr int kThreads = (4 + kEpiWarps) * 32;
   static constexpr int kRoleRegs = 56, kEpiRegs = 224;  // WIDE
   static_assert(!WIDE || (kThreads == 384 && kRoleRegs * 128 + kEpiRegs * 256 <= 168 * 384), "register split");
+  // Steps that the tensor cores sum in TMEM before the epilogue adds them to its registers: one
+  // scale block in e4m3; all of K where D is rounded to bf16; four, 256 rows, in Dw, whose
+  // fp32 result would show more (the tensor cores' adder cuts off where an fp32 addition
+  // rounds, so the error grows with the additions in a row: over 16384 rows 1.9e-5 of dW's
+  // norm summed in one go, 2.7e-7 so, 3.7e-7 by an fp32 product; 191 against 198 us at 8192
+  // rows, 4096 x 4096).
+  static constexpr int kSum = F8 ? 1 : DW ? 4 : 1 << 30;
   static constexpr int kBufs = F8 ? 512 / BN : 2;       // TMEM buffers of BN columns
   static constexpr int kTmemCols = kBufs * BN;
   static constexpr int kPassCols = DW ? 32 : 64;        // D columns in 128 bytes
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
         for (int kb = 0; kb < x.nk; ++kb) {
           const uint32_t buf = u % C::kBufs;
-          if (C::F8 || kb == 0) {
+          if (kb % C::kSum == 0) {
             if (!mbar_wait_lazy(tempty_bar(buf), ((u / C::kBufs) & 1u) ^ 1u)) {
               set_status_site(p.status, QLORA_ERR_TIMEOUT, 63);
               ok = false;
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
           for (uint32_t kk = 0; kk < 4; ++kk) {
             const uint64_t a2 = ad + uint64_t((kk * a_adv) >> 4), b2 = bd + uint64_t((kk * b_adv) >> 4);
-            const uint32_t acc = (kk > 0 || (!C::F8 && kb > 0)) ? 1u : 0u;
+            const uint32_t acc = (kk > 0 || kb % C::kSum > 0) ? 1u : 0u;
             if constexpr (C::PAIR) {
               if constexpr (C::F8) tc_mma_f8_pair(d, a2, b2, idesc, acc);
               else tc_mma_bf16_pair(d, a2, b2, idesc, acc);
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           if constexpr (C::PAIR) tc_commit_pair_mc(empty_bar(s), 3);
           else tc_commit(empty_bar(s));
-          if (C::F8 || kb == x.nk - 1) {
+          if (kb % C::kSum == C::kSum - 1 || kb == x.nk - 1) {
             if constexpr (C::PAIR) tc_commit_pair_mc(tfull_bar(buf), 3);
             else tc_commit(tfull_bar(buf));
             ++u;
@@ -570,7 +578,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
         }
       } else {
-        if (x.nk > 0) take(1.f);
+        for (int k = 0; k < x.nk && ok; k += C::kSum) take(1.f);
       }
       if (!ok) break;
       if (rows <= 0) continue;

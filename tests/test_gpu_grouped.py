@@ -126,6 +126,19 @@ def test_nan_of_one_expert_stays_there(cuda_device, kind):
         assert torch.equal(dW[[0, 2]], clean[2][[0, 2]])
 
 
+@pytest.mark.parametrize("M", [1000, 16384])
+def test_dw_over_many_rows(cuda_device, M):
+    """dW is summed in fp32 in spans of 256 rows: within a span the tensor cores make 16 additions that may cut off
+    up to a whole last place (2^-23) of the partial sum, so a span is off by at most 16 2^-23 of its norm and spans of
+    independent errors together by no more; the additions of the spans round, by 2^-24 each of a growing sum."""
+    X, dY = normal((M, 256), 1).to(cuda_device), normal((M, 192), 2).to(cuda_device)
+    W = torch.zeros((1, 192, 256), dtype=torch.bfloat16, device=cuda_device)
+    offs = torch.tensor([0, M], dtype=torch.int32, device=cuda_device)
+    _, dW = api.grouped_linear_bwd(W, X, dY, offs, need_dX=False)
+    ref = f64(dY).T @ f64(X)
+    assert np.linalg.norm(f64(dW[0]) - ref) <= 16 * 2.0 ** -23 * np.linalg.norm(ref)
+
+
 def test_no_rows_at_all(cuda_device):
     """Every group empty: nothing is written but dW, which is zero."""
     X, dY, W = (normal(s, 1).to(cuda_device) for s in ((4, 32), (4, 48), (3, 48, 32)))

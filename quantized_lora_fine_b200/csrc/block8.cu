@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows8_kernel(const uint1
     const int64_t b = b0 + j * (kRowThreads / 16);
     float f[8];
     bf16x8_to_f32(v[j], f);
-    const Block8 q = block8_of(max16(max_abs8(f)));
+    const Block8 q = block8_of(max16(max_abs8(v[j])));
     if (at[j] >= 0) *reinterpret_cast<uint2*>(codes + at[j]) = quantize8(f, q);
     if (b < blocks && sub == 0) scale[b] = q.scale;
   }

@@ -5,12 +5,13 @@
 //   q = e4m3_rne(448 x / a) of the real quotient.
 //
 // The quotient is decided in fp32: with p = 2^-exponent(a), a' = a p is in [1, 2) and
-// u = 448 p x (both exact for bf16 x: 8 + 3 significant bits), and t = u * rn(1 / a')
-// is corrected once by its remainder, t + (u - t a') * rn(1 / a') (Markstein's
-// quotient step), which returns the real quotient wherever it is representable. So a
-// quotient that lies on the midpoint of two e4m3 values is seen as the midpoint and
-// rounds to even; no other quotient of two bf16 values is within fp32 rounding of one.
-// A block that holds a NaN or an infinity gets NaN codes.
+// u = 448 p x (both exact for bf16 x: 8 + 3 significant bits), t = u y with y near 1 / a', and t is
+// corrected once by its remainder, t + (u - t a') y (Markstein's quotient step; the
+// remainder is exact, so y needs no more than a few last places). That returns the real
+// quotient wherever it is representable, so a quotient on the midpoint of two e4m3 values
+// is seen as the midpoint and rounds to even; no other quotient of two bf16 values is within
+// fp32 rounding of one. The scale is the same step with 448. A block that holds a NaN or an
+// infinity gets NaN codes: its p is infinite.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -26,7 +27,7 @@ struct Block8 {
   float scale;   // a / 448
   float c;       // 448 * 2^-exponent(a)
   float a;       // a', in [1, 2)
-  float inv;     // 1 / a'
+  float inv;     // near 1 / a'
 };
 
 // `bits`: the largest |x| of the block as fp32 bits (as integers, so that NaN > Inf >
@@ -35,17 +36,15 @@ __device__ __forceinline__ Block8 block8_of(uint32_t bits) {
   bits = max(bits, kBlock8Floor);
   Block8 b;
   const float a = __uint_as_float(bits);
-  b.scale = __fdiv_rn(a, 448.f);
-  if (bits >= 0x7F800000u) {
-    b.c = b.a = b.inv = __uint_as_float(0x7FC00000u);
-    return b;
-  }
-  const uint32_t e = bits >> 23;                          // 27 .. 254
-  const float p = e == 254u ? __uint_as_float(0x00400000u)   // 2^-127
-                            : __uint_as_float((254u - e) << 23);
-  b.c = 448.f * p;
+  constexpr float r448 = 1.f / 448.f;
+  const float t = __fmul_rn(a, r448);
+  b.scale = bits < 0x7F800000u ? __fmaf_rn(__fmaf_rn(-t, 448.f, a), r448, t) : a;
+  // 2^-exponent(a): the exponent's complement; 2^-127, subnormal, for the largest; a NaN's or
+  // infinity's (e = 255) comes out as -infinity.
+  const uint32_t e = bits >> 23;                          // 27 .. 255
+  b.c = 448.f * __uint_as_float(max((254u - e) << 23, 0x00400000u));
   b.a = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
-  b.inv = __frcp_rn(b.a);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.inv) : "f"(b.a));
   return b;
 }
 
@@ -77,6 +76,13 @@ __device__ __forceinline__ uint32_t max_abs8(const float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
   return m;
+}
+
+// The same of 8 bf16 values: magnitudes as 16-bit integers, two at a time.
+__device__ __forceinline__ uint32_t max_abs8(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                              __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
 // Over 16 consecutive lanes (one 128-value block at 8 values a lane).

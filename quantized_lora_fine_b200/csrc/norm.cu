@@ -50,7 +50,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // One CTA per row; thread t holds the 8-value vectors t, t + T, ... (VPT of them), so 16
 // neighbouring lanes hold one 128-value block.
 template <int VPT, bool WF32>
-__global__ void __launch_bounds__(512) rms_norm_fwd_kernel(NormFwd a) {
+__global__ void __launch_bounds__(512, VPT <= 2 ? 3 : 1) rms_norm_fwd_kernel(NormFwd a) {
   __shared__ float s_part[32];
   const int T = blockDim.x, nv = int(a.H >> 3);
   const int64_t row = blockIdx.x;
@@ -84,6 +84,14 @@ __global__ void __launch_bounds__(512) rms_norm_fwd_kernel(NormFwd a) {
     const int i = int(threadIdx.x) + j * T;
     if (a.h && i < nv) reinterpret_cast<uint4*>(a.h + row * a.H)[i] = v[j];
   }
+  uint4 wv[VPT];
+  if constexpr (!WF32) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = int(threadIdx.x) + j * T;
+      wv[j] = i < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + i) : make_uint4(0, 0, 0, 0);
+    }
+  }
   ss = cta_sum(ss, s_part);
   const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, float(a.H)) + a.eps));
   if (threadIdx.x == 0) a.rstd[row] = rstd;
@@ -93,7 +101,8 @@ __global__ void __launch_bounds__(512) rms_norm_fwd_kernel(NormFwd a) {
     float f[8], w[8];
     bf16x8_to_f32(v[j], f);
     if (i < nv) {
-      load_w8<WF32>(a.w, int64_t(i) * 8, w);
+      if constexpr (WF32) load_w8<WF32>(a.w, int64_t(i) * 8, w);
+      else bf16x8_to_f32(wv[j], w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = f[k] * rstd * w[k];
       if (a.y) reinterpret_cast<uint4*>(a.y + row * a.H)[i] = pack8(f);

@@ -458,7 +458,7 @@ qlora_status nf4_layer_error_rank_noalloc(int32_t n_layers, const uint16_t* cons
  * [experts][ceil(out / 128)][ceil(in / 128)]; the last blocks may be short.
  *
  * `in` and `out` are multiples of 16 up to 2^24, M is 1 .. 2^30, any value in
- * between. These calls use a workspace only where they take one; calls on
+ * between. Outputs may not overlap inputs unless a call says so. These calls use a workspace only where they take one; calls on
  * several streams may share a status workspace (qlora_expert_workspace_size()
  * bytes: the status word alone, zeroed once). */
 

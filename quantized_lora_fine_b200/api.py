@@ -633,11 +633,21 @@ def _rows_of(rows, eight_bit: bool, cols: int, name: str):
     return t, sc, dev
 
 
-def _output(t: Optional[torch.Tensor], shape: tuple, dtype, like: torch.Tensor, dev: int, name: str) -> torch.Tensor:
+def _output(t: Optional[torch.Tensor], shape: tuple, dtype, dev: int, name: str, *inputs) -> torch.Tensor:
+    """A new output, or the caller's, which may not share memory with an input (the first one has the
+    device)."""
     if t is None:
-        return torch.empty(*shape, dtype=dtype, device=like.device)
+        return torch.empty(*shape, dtype=dtype, device=inputs[0].device)
     _check(t, dtype, shape, name, dev)
+    a, b = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    for i in inputs:
+        if i is not None and i.data_ptr() < b and a < i.data_ptr() + i.numel() * i.element_size():
+            raise ValueError(f"{name} may not overlap an input of the call")
     return t
+
+
+def _parts(W) -> tuple:
+    return (W.codes, W.scale) if isinstance(W, FP8Weight) else (W,)
 
 
 def fp8_linear_fwd(w: FP8Weight, X, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -656,7 +666,7 @@ def fp8_linear_fwd(w: FP8Weight, X, Y: Optional[torch.Tensor] = None) -> torch.T
         q = fp8_quantize_rows(x)
         x, sx = q.codes, q.scale
     ws = _status_ptr(dev)
-    Y = _output(Y, (M, w.out), _BF16, x, dev, "Y")
+    Y = _output(Y, (M, w.out), _BF16, dev, "Y", x, sx, w.codes, w.scale)
     check(lib.fp8_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), M, Y.data_ptr(), ws, 256,
                              _raw_stream(dev)), "fp8_linear_fwd")
     return Y
@@ -680,7 +690,7 @@ def fp8_linear_bwd(w: FP8Weight, dY, dX: Optional[torch.Tensor] = None) -> torch
         q = fp8_quantize_rows(d)
         d, sd = q.codes, q.scale
     ws = _status_ptr(dev)
-    dX = _output(dX, (d.shape[0], w.inp), _BF16, d, dev, "dX")
+    dX = _output(dX, (d.shape[0], w.inp), _BF16, dev, "dX", d, sd, w.codes, w.scale)
     check(_lib.load().fp8_linear_bwd(ctypes.byref(cs), d.data_ptr(), sd.data_ptr(), d.shape[0], dX.data_ptr(),
                                      ws, 256, _raw_stream(dev)), "fp8_linear_bwd")
     return dX
@@ -702,7 +712,7 @@ def grouped_linear_fwd(W, X, offsets: torch.Tensor, Y: Optional[torch.Tensor] = 
         q = fp8_quantize_rows(x)
         x, sx = q.codes, q.scale
     ws = _status_ptr(dev)
-    Y = _output(Y, (x.shape[0], o), _BF16, x, dev, "Y")
+    Y = _output(Y, (x.shape[0], o), _BF16, dev, "Y", x, sx, *_parts(W), offsets)
     check(_lib.load().qlora_grouped_linear_fwd(ctypes.byref(cs), x.data_ptr(), _ptr(sx), x.shape[0],
                                                offsets.data_ptr(), Y.data_ptr(), ws, 256,
                                                _raw_stream(dev)), "qlora_grouped_linear_fwd")
@@ -736,8 +746,8 @@ def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, 
         q = fp8_quantize_rows(d)
         d, sd = q.codes, q.scale
     ws = _status_ptr(dev)
-    dX = _output(dX, (M, i), _BF16, d, dev, "dX") if need_dX else None
-    dW = _output(dW, (E, o, i), _F32, d, dev, "dW") if need_dW else None
+    dX = _output(dX, (M, i), _BF16, dev, "dX", d, sd, *_parts(W), offsets, X if need_dW else None) if need_dX else None
+    dW = _output(dW, (E, o, i), _F32, dev, "dW", d, X, offsets, dX) if need_dW else None
     check(_lib.load().qlora_grouped_linear_bwd(ctypes.byref(cs), xp, d.data_ptr(), _ptr(sd), M, offsets.data_ptr(),
                                                _ptr(dX), _ptr(dW), ws, 256, _raw_stream(dev)),
           "qlora_grouped_linear_bwd")
@@ -746,9 +756,12 @@ def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, 
 
 def status() -> int:
     """First nonzero device status word among this device's workspaces (one per
-    stream the library was called on); synchronizes."""
+    stream the library was called on, and one for the calls that share it);
+    synchronizes."""
     idx = torch.cuda.current_device()
     dev = torch.device("cuda", idx)
+    if (idx, None) in Workspace._bufs:
+        torch.cuda.synchronize(idx)      # that word is every stream's
     for ws in Workspace.all(idx) or [Workspace.get(256, dev)]:
         st = read_status(ws)
         if st:

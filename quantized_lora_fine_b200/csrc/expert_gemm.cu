@@ -443,7 +443,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       it += x.nk;
       const int valid = x.k_rows - (x.nk - 1) * C::BK;
       if (x.nk == 0 || valid == C::BK) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait_lazy(tail_bar(ntail % C::STAGES), (ntail / C::STAGES) & 1u))) {
+      // (a whole tile's steps may pass before: 4 us for each are ten times what they take)
+      const uint64_t limit = 2000000000ull + 4000ull * uint64_t(x.nk);
+      if (!__all_sync(0xffffffffu, mbar_wait_lazy(tail_bar(ntail % C::STAGES), (ntail / C::STAGES) & 1u, limit))) {
         if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 62);
         break;
       }
@@ -660,6 +662,14 @@ int resident_units() {
   if (n > 0) return n;
   if (cudaFuncSetAttribute(expert_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return 0;
+  if (C::WIDE) {
+    // The warpgroups' shares after the split have to fit in what the block is launched with:
+    // one that asks for more would wait for good.
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, expert_gemm_kernel<C>) != cudaSuccess ||
+        fa.numRegs * C::kThreads < C::kRoleRegs * 128 + C::kEpiRegs * 256)
+      return 0;
+  }
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
   n = sms;

@@ -170,3 +170,47 @@ def test_one_expert_of_a_2d_weight(cuda_device):
     X, W = normal((77, 64), 1).to(cuda_device), normal((48, 64), 2).to(cuda_device)
     offs = torch.tensor([0, 77], dtype=torch.int32, device=cuda_device)
     assert_product(f64(api.grouped_linear_fwd(W, X, offs)), f64(X), f64(W).T, "Y")
+
+
+def test_refused_calls(cuda_device):
+    """What the binding refuses in words: shapes, types, kinds that do not go together, overlapping outputs."""
+    W, X = normal((2, 64, 64), 1).to(cuda_device), normal((5, 64), 2).to(cuda_device)
+    offs = torch.tensor([0, 2, 5], dtype=torch.int32, device=cuda_device)
+    w8, x8 = api.fp8_quantize_weight(W), api.fp8_quantize_rows(X)
+    bad = [
+        (lambda: api.grouped_linear_fwd(W, x8, offs), "FP8Weight"),
+        (lambda: api.grouped_linear_fwd(W, X[:, :32].contiguous(), offs), "columns"),
+        (lambda: api.grouped_linear_fwd(W, X, offs.long()), "int32"),
+        (lambda: api.grouped_linear_fwd(W, X, offs[:2]), "shape"),
+        (lambda: api.grouped_linear_fwd(W, X, offs.cpu()), "CUDA"),
+        (lambda: api.grouped_linear_fwd(W, X.float(), offs), "bfloat16"),
+        (lambda: api.grouped_linear_fwd(W, X.t().contiguous().t(), offs), "contiguous"),
+        (lambda: api.grouped_linear_fwd(W, X, offs, Y=X), "overlap"),
+        (lambda: api.grouped_linear_bwd(W, X, X, offs, dX=X), "overlap"),
+        (lambda: api.grouped_linear_bwd(W, X, X, offs, need_dX=False, need_dW=False), "must be true"),
+        (lambda: api.grouped_linear_bwd(W, None, X, offs), "X is needed"),
+        (lambda: api.grouped_linear_bwd(w8, X, X, offs), "frozen"),
+        (lambda: api.fp8_linear_fwd(w8, X), "FP8Weight"),
+        (lambda: api.FP8Rows(x8.codes, x8.scale[:4].contiguous()), "shape"),
+        (lambda: api.FP8Weight(w8.codes, w8.scale[0]), "shape"),
+    ]
+    for call, words in bad:
+        with pytest.raises(ValueError, match=words):
+            call()
+    with pytest.raises(RuntimeError, match="QLORA_ERR_SHAPE"):      # 40 is no multiple of 16
+        api.grouped_linear_fwd(normal((2, 64, 40), 1).to(cuda_device), normal((5, 40), 2).to(cuda_device), offs)
+    with pytest.raises(RuntimeError, match="QLORA_ERR_SHAPE"):      # no rows
+        api.grouped_linear_fwd(W, X[:0], offs)
+    with pytest.raises(RuntimeError, match="QLORA_ERR_ALIGN"):
+        api.grouped_linear_fwd(W, normal((5 * 64 + 1,), 3).to(cuda_device)[1:].view(5, 64), offs)
+
+
+def test_rows_and_scales_at_any_start(cuda_device):
+    """Slices of larger tensors: rows from an odd one on, scales that start on no 16 bytes."""
+    x = api.fp8_quantize_rows(normal((40, 640), 1).to(cuda_device))
+    w = api.fp8_quantize_weight(normal((64, 640), 2, 0.05).to(cuda_device))
+    W = blocks.weight_values(f64(w.codes), f64(w.scale).astype(np.float32))
+    for first in (1, 3, 20):
+        q = api.FP8Rows(x.codes[first:], x.scale[first:])
+        X = blocks.row_values(f64(q.codes), f64(q.scale).astype(np.float32))
+        assert_product(f64(api.fp8_linear_fwd(w, q)), X, W.T, "Y")

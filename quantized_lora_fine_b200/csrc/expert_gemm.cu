@@ -44,6 +44,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -64,6 +65,7 @@ struct ExpertParams {
   int tiles_n;           // ceil(n_cols / BN)
   int tiles_r;           // Dw: row tiles of D per expert
   int nk;                // K steps (Fwd, Dx)
+  int split, k_part;     // SPLIT: CTAs a tile, K steps of each (a multiple of 4)
   int d_rows;            // Dw: rows of D per expert
   int a_box;             // rows of A per TMA box: 128, or 32 where groups are small
   const int32_t* offsets;
@@ -78,10 +80,12 @@ struct ExpertParams {
   int* status;
 };
 
-template <bool PAIR_, int BN_, bool F8_, ExpertMode MODE_>
+template <bool PAIR_, int BN_, bool F8_, ExpertMode MODE_, bool SPLIT_ = false>
 struct ExpertCfg {
   static constexpr bool PAIR = PAIR_, F8 = F8_, WIDE = BN_ == 256;
+  static constexpr bool SPLIT = SPLIT_;                 // K over a cluster of 2, 4 or 8 CTAs
   static_assert(WIDE || (BN_ == 128 && !PAIR), "tile widths");
+  static_assert(!SPLIT || (!WIDE && MODE_ != ExpertMode::Dw), "K is split in 128 x 128 tiles");
   static constexpr ExpertMode MODE = MODE_;
   static constexpr bool DW = MODE == ExpertMode::Dw;
   static constexpr bool A_MN = DW, B_MN = MODE != ExpertMode::Fwd;
@@ -119,6 +123,9 @@ struct ExpertCfg {
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kSmem = kTableOff + 2 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
+  // SPLIT: one warp's sums, 32 lanes x kCols fp32, from one of the other CTAs.
+  static constexpr int kPart = 32 * kCols * 4;
+  static_assert(!SPLIT || kEpiWarps * kPart <= STAGES * kStage, "room for the parts");
 };
 
 // acc += v * s for two values at once.
@@ -130,12 +137,18 @@ __device__ __forceinline__ uint64_t dup2(float s) {
   asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
   return r;
 }
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
 __device__ __forceinline__ void unpack2(uint64_t a, uint32_t& lo, uint32_t& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(a));
 }
 
 struct ExpertTile {
   int e, n0, nk;
+  int kb0;            // SPLIT: this CTA's first step (0 otherwise); nk counts from it
   int row0, rows;     // Fwd, Dx: first row of the tile in A and D, rows of the group from there
                       // Dw: first row of D in the expert, rows of D from there
   int k_row0, k_rows; // Dw: the group's rows
@@ -156,6 +169,7 @@ template <class C>
 __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, const int* starts, const int* tiles, int t,
                                                   int& e) {
   ExpertTile x;
+  x.kb0 = 0;
   if constexpr (C::DW) {
     const int per = p.tiles_r * p.tiles_n;
     e = t / per;
@@ -176,6 +190,10 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, const i
     x.rows = starts[e + 1] - x.row0;
     x.n0 = n * C::BN;
     x.nk = p.nk;
+    if constexpr (C::SPLIT) {
+      x.kb0 = min(p.nk, int(cluster_ctarank()) * p.k_part);
+      x.nk = min(p.k_part, p.nk - x.kb0);
+    }
     x.k_row0 = x.k_rows = 0;
   }
   x.e = e;
@@ -205,8 +223,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = C::PAIR ? cluster_ctarank() : 0u;
-  const int unit = C::PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
-  const int units = C::PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
+  // (SPLIT: as many clusters as tiles, so each loop over tiles below runs at most once.)
+  const int unit = C::PAIR ? int(blockIdx.x >> 1) : C::SPLIT ? int(blockIdx.x) / p.split : int(blockIdx.x);
+  const int units = C::PAIR ? int(gridDim.x >> 1) : C::SPLIT ? int(gridDim.x) / p.split : int(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -329,7 +348,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             bar = full_bar(s);
             mbar_arrive_expect_tx(bar, (C::A_MN ? C::kA : boxes * p.a_box * 128) + C::kB);
           }
-          const int k0 = kb * C::BK;
+          const int k0 = (x.kb0 + kb) * C::BK;
           auto load2 = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy) {
             if (C::PAIR && !tail) tma_load_2d_pair(dst, m, bar, cx, cy);
             else tma_load_2d(dst, m, bar, cx, cy);
@@ -476,9 +495,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       for (int t = unit; t < num_tiles && ok; t += units) {
         const ExpertTile x = expert_tile<C>(p, starts, tiles, t, e);
         const int r0 = int(rank) * 128 + t0;
-        const float* ra = p.sa + int64_t(x.row0 + min(r0, x.rows - 1)) * p.nb_a;
-        const float* rb = p.sa + int64_t(x.row0 + min(r0 + 64, x.rows - 1)) * p.nb_a;
-        const float* sb = p.sb + x.e * p.sb_e;
+        const float* ra = p.sa + int64_t(x.row0 + min(r0, x.rows - 1)) * p.nb_a + x.kb0;
+        const float* rb = p.sa + int64_t(x.row0 + min(r0 + 64, x.rows - 1)) * p.nb_a + x.kb0;
+        const float* sb = p.sb + x.e * p.sb_e + x.kb0 * p.sb_k;
         for (int k0 = 0; k0 < x.nk; k0 += 4, ++g) {
           const int s = g % C::kScaleSlots;
           float a[2][4], w[C::kBlocksN][4];
@@ -515,6 +534,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
     }
+  }
+  if constexpr (C::SPLIT) {
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -582,6 +606,39 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       } else {
         for (int k = 0; k < x.nk && ok; k += C::kSum) take(1.f);
       }
+      if constexpr (C::SPLIT) {
+        // Each CTA finishes the warps w = its rank (mod the cluster's CTAs): the others send it
+        // those warps' sums, into its ring, which is idle once every CTA is past its products,
+        // and it adds them to its own in the order of their ranks.
+        const int krank = int(cluster_ctarank()), w = int(warp) - 4;
+        const int owner = w % p.split, per = C::kEpiWarps / p.split;
+        auto slot = [&](int from) { return base + uint32_t(from * per + w / p.split) * C::kPart + lane * 16u; };
+        cluster_sync();
+        if (owner != krank && rows > 0) {
+          const uint32_t dst = mapa_shared(slot(krank - (krank > owner)), owner);
+#pragma unroll
+          for (int i = 0; i < C::kCols / 4; ++i) {
+            uint4 o;
+            unpack2(acc[2 * i], o.x, o.y);
+            unpack2(acc[2 * i + 1], o.z, o.w);
+            st_cluster_u4(dst + i * 512, o);
+          }
+        }
+        cluster_sync();
+        if (owner != krank) break;
+        if (rows > 0) {
+          for (int r = 0; r + 1 < p.split; ++r) {
+            const uint32_t src = slot(r);
+#pragma unroll
+            for (int i = 0; i < C::kCols / 4; ++i) {
+              uint32_t v[4];
+              lds_u4(src + i * 512, v);
+              fma2(acc[2 * i], pack2(v[0], v[1]), dup2(1.f));
+              fma2(acc[2 * i + 1], pack2(v[2], v[3]), dup2(1.f));
+            }
+          }
+        }
+      }
       if (!ok) break;
       if (rows <= 0) continue;
       // Through this warp's staging buffers (128-byte swizzle) to global memory: by TMA, or row
@@ -635,6 +692,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
     }
     if (lane == 0) bulk_wait_group<0>();
+    if constexpr (C::SPLIT) {
+      if (unit >= num_tiles) {      // no tile: the barriers that the others pass
+        cluster_sync();
+        cluster_sync();
+      }
+    }
   }
 
   tc_fence_before();
@@ -695,8 +758,16 @@ int resident_units() {
   return n;
 }
 
+// K steps of each CTA of a cluster that splits nk of them (whole groups of four scales).
+int split_part(int nk, int split) { return ((nk + split - 1) / split + 3) / 4 * 4; }
+
+// Row tiles at most: every group may end inside a tile.
+int64_t most_row_tiles(const ExpertArgs& a, int bm) {
+  return std::min<int64_t>(a.M, (a.M + bm - 1) / bm + (a.offsets ? a.E - 1 : 0));
+}
+
 template <class C>
-qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
+qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s, int split = 1) {
   const int max_units = resident_units<C>();
   if (max_units <= 0) return QLORA_ERR_CUDA;
   const TmapType ty = C::F8 ? TmapType::U8 : TmapType::BF16;
@@ -711,6 +782,8 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
   p.tiles_n = int((N + C::BN - 1) / C::BN);
   p.tiles_r = int((a.out + C::BM - 1) / C::BM);
   p.nk = int((K + C::BK - 1) / C::BK);
+  p.split = split;
+  p.k_part = split_part(p.nk, split);
   p.d_rows = int(a.out);
   // Groups of a few rows: boxes of 32 rows, so that a tile's unused rows are not fetched.
   p.a_box = (!C::PAIR && a.M < 64 * a.E) ? 32 : 128;
@@ -741,27 +814,25 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s) {
   }
   if (!good) return QLORA_ERR_CUDA;
 
-  // Row tiles at most: every group may end inside a tile.
-  const int64_t row_tiles = dw ? a.E * p.tiles_r
-                               : std::min<int64_t>(a.M, (a.M + C::BM - 1) / C::BM + (a.offsets ? a.E - 1 : 0));
-  const int64_t num_tiles = row_tiles * p.tiles_n;
+  const int64_t num_tiles = dw ? a.E * p.tiles_r * p.tiles_n : most_row_tiles(a, C::BM) * p.tiles_n;
   if (num_tiles > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;
   const int units = int(std::min<int64_t>(num_tiles, max_units));
+  if (C::SPLIT && num_tiles * split > max_units) return QLORA_ERR_SHAPE;   // one tile a cluster
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = C::PAIR ? 2 : unsigned(split);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(units * (C::PAIR ? 2 : 1)), 1, 1);
+  cfg.gridDim = dim3(unsigned(units * (C::PAIR ? 2 : split)), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   const int skip = pdl_enabled() ? 0 : 1;
   cfg.attrs = attr + skip;
-  cfg.numAttrs = (C::PAIR ? 2 : 1) - skip;
+  cfg.numAttrs = (C::PAIR || C::SPLIT ? 2 : 1) - skip;
   if (cudaLaunchKernelEx(&cfg, expert_gemm_kernel<C>, A, B, D, p) != cudaSuccess) {
     cudaGetLastError();
     return QLORA_ERR_CUDA;
@@ -805,9 +876,9 @@ ExpertTileKind tile_kind(const ExpertArgs& a) {
   auto cost = [&](int bm, int bn, int at_once, double step) {
     const int64_t cols = (N + bn - 1) / bn;
     if (!a.offsets) return double(((a.M + bm - 1) / bm * cols + at_once - 1) / at_once) * step;
-    const double rows = std::max(double(std::min(a.E, a.M)), double(a.M) / bm + 0.5 * double(a.E));
+    const double rows = std::max(double(std::min(a.E, a.M)), std::ceil(double(a.M) / bm) + 0.5 * double(a.E - 1));
     const double waves = rows * double(cols) / at_once;
-    return (waves <= 0.9 ? 1.0 : waves + 0.5) * step;
+    return (a.E == 1 ? std::ceil(waves) : waves <= 0.9 ? 1.0 : waves + 0.5) * step;
   };
   const double c128 = cost(128, 128, 148, F8 ? 0.40 : 0.27), c256 = cost(128, 256, 148, F8 ? 0.64 : 0.52),
                cpair = cost(256, 256, 74, F8 ? 0.61 : 0.386);
@@ -815,13 +886,34 @@ ExpertTileKind tile_kind(const ExpertArgs& a) {
   return c256 <= c128 ? ExpertTileKind::T256 : ExpertTileKind::T128;
 }
 
+// CTAs that share a 128 x 128 tile's K: where even the most tiles that there can be leave SMs
+// idle, each CTA keeps eight steps, and all clusters run at once (16 of 8 CTAs do not: 22.9 us
+// where 16 of 4 took 16.9, e4m3 at 256 rows, 1024 x 11008). e4m3 at 64 rows, 4096 x 4096: 9.7 us by four CTAs,
+// 14.7 by one; 4096 x 11008: 17.1 and 35; at 256 rows by two: 13.4 and 15.9. bf16 at 17 rows,
+// 4096 x 4096: 10.1 by four.
+template <bool F8>
+int split_of(const ExpertArgs& a) {
+  const bool fwd = a.mode == ExpertMode::Fwd;
+  const int64_t N = fwd ? a.out : a.in, K = fwd ? a.in : a.out;
+  const int64_t tiles = most_row_tiles(a, 128) * ((N + 127) / 128);
+  const int64_t nk = (K * (F8 ? 1 : 2) + 127) / 128;
+  if (tiles <= 8 && nk >= 64) return 8;
+  if (tiles <= 32 && nk >= 32) return 4;
+  return tiles <= 74 && nk >= 16 ? 2 : 1;
+}
+
 template <bool F8, ExpertMode MODE>
 qlora_status launch_mode(const ExpertArgs& a, cudaStream_t s) {
   switch (tile_kind<F8>(a)) {
     case ExpertTileKind::Pair: return launch_cfg<ExpertCfg<true, 256, F8, MODE>>(a, s);
     case ExpertTileKind::T256: return launch_cfg<ExpertCfg<false, 256, F8, MODE>>(a, s);
-    default: return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
+    default: break;
   }
+  if constexpr (MODE != ExpertMode::Dw) {
+    const int split = split_of<F8>(a);
+    if (split > 1) return launch_cfg<ExpertCfg<false, 128, F8, MODE, true>>(a, s, split);
+  }
+  return launch_cfg<ExpertCfg<false, 128, F8, MODE>>(a, s);
 }
 
 }  // namespace

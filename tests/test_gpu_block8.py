@@ -119,6 +119,13 @@ def test_linear_larger(cuda_device, M, o, i):
     _linear(cuda_device, M, o, i)
 
 
+@pytest.mark.parametrize("M", [17, 100, 130, 500])
+@pytest.mark.parametrize("o,i", [(144, 4112), (4112, 144), (1040, 2048), (16, 11008), (2176, 2560)])
+def test_linear_split_over_k(cuda_device, M, o, i):
+    """Few tiles of a long K: 2, 4 or 8 CTAs share a tile's K, the last of them with fewer steps or none."""
+    _linear(cuda_device, M, o, i)
+
+
 @pytest.mark.parametrize("tile", ["128", "256", "pair"])
 @pytest.mark.parametrize("M,o,i", [(1, 16, 16), (9, 272, 144), (129, 528, 1040), (300, 1024, 2048), (2048, 2064, 512)])
 def test_linear_every_tile(cuda_device, monkeypatch, tile, M, o, i):

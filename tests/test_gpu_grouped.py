@@ -89,6 +89,14 @@ def test_few_rows_a_group(cuda_device, sizes, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("sizes", [[30, 0, 130], [0, 0, 40], [200], [1, 33, 15, 0, 40]])
+@pytest.mark.parametrize("o,i", [(144, 4112), (2576, 272)])
+def test_split_over_k(cuda_device, sizes, o, i, kind):
+    """Few tiles of a long K, some clusters without a tile."""
+    _run(cuda_device, sizes, o, i, kind, before=2, after=3)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("groups", ["with empty", "step edges", "large"])
 def test_rows_outside_groups(cuda_device, groups, kind):
     """Rows before the first and behind the last group are neither read into a sum nor written."""

@@ -588,20 +588,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       };
       if constexpr (C::F8) {
-        for (int k = 0; k < x.nk && ok; ++k) {
+        for (int k = 0; k < x.nk && ok; k += 4, ++g) {
           const uint32_t slot = g % C::kScaleSlots;
-          if (k % 4 == 0 && !__all_sync(0xffffffffu, mbar_wait_lazy(sfull_bar(slot), (g / C::kScaleSlots) & 1u))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_lazy(sfull_bar(slot), (g / C::kScaleSlots) & 1u))) {
             if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 67);
             ok = false;
           }
-          const float f = reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScaleSlot)
-              [((k & 3) * C::kBlocksN + cg * C::kCols / 128) * 128 + q * 32 + lane];
-          take(f);
-          if (k % 4 == 3 || k == x.nk - 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sempty_bar(slot));
-            ++g;
+          const uint32_t f = base + C::kScaleOff + slot * C::kScaleSlot +
+                             ((cg * C::kCols / 128) * 128 + q * 32 + lane) * 4;
+          const int n = min(4, x.nk - k);
+          // Four in a row without a loop between them where the registers last: at 2048 rows,
+          // 4096 x 4096, 40.5 us in 128 x 128 tiles against 48.5 (53 with the tests of each step in
+          // the loop); 256-column tiles would spill (61 us against 40).
+          if (!C::WIDE && n == 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) take(lds_f32(f + j * C::kBlocksN * 512));
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) take(lds_f32(f + j * C::kBlocksN * 512));
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty_bar(slot));
         }
       } else {
         for (int k = 0; k < x.nk && ok; k += C::kSum) take(1.f);
@@ -844,11 +851,11 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s, int split = 1) {
 // with full waves (us per step of 128 bytes of K; bf16 128 x 256 a tenth above its rate with
 // operands in L2, for the weights of groups come from HBM):
 //                  e4m3    bf16
-//   128 x 128      0.40    0.27     148 at once; the most units and the fewest wasted rows
+//   128 x 128      0.33    0.27     148 at once; the most units and the fewest wasted rows
 //   128 x 256      0.64    0.52     148 at once
 //   256 x 256 pair 0.61    0.386    74 at once; half the L2 bytes of 128 x 128 per product
-// (e4m3 4096 x 4096 at 512 rows: 15.9, 21.4 and 21.4 us; at 2048: 54, 41 and 41; at 8192: 177,
-// 142 and 136. bf16 at 8192: 251, 207 and 173.) Groups' sizes are on the device: their row
+// (e4m3 4096 x 4096 at 512 rows: 12.6, 20.4 and 21.5 us; at 2048: 40.5, 39.5 and 40; at 8192:
+// 148, 140 and 136. bf16 at 8192: 251, 207 and 173.) Groups' sizes are on the device: their row
 // tiles are taken as half a tile more than full for each group, and the waves, where they
 // are not safely one, as half a wave more (16 experts of 1408 x 2048 in bf16, 128 rows each
 // on average: 25, 36 and 29 us; 64 of 1024 x 2048, 256 rows each: 99, 97 and 82).
@@ -880,7 +887,7 @@ ExpertTileKind tile_kind(const ExpertArgs& a) {
     const double waves = rows * double(cols) / at_once;
     return (a.E == 1 ? std::ceil(waves) : waves <= 0.9 ? 1.0 : waves + 0.5) * step;
   };
-  const double c128 = cost(128, 128, 148, F8 ? 0.40 : 0.27), c256 = cost(128, 256, 148, F8 ? 0.64 : 0.52),
+  const double c128 = cost(128, 128, 148, F8 ? 0.33 : 0.27), c256 = cost(128, 256, 148, F8 ? 0.64 : 0.52),
                cpair = cost(256, 256, 74, F8 ? 0.61 : 0.386);
   if (cpair <= c256 && cpair <= c128) return ExpertTileKind::Pair;
   return c256 <= c128 ? ExpertTileKind::T256 : ExpertTileKind::T128;

@@ -257,13 +257,12 @@ qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s)
   p.nk = (p.wbytes + 127) / 128;
   p.nb_n = int((a.out + 127) / 128);
   const dim3 grid(unsigned(a.out / 16), unsigned(a.E)), block(kFewWarps * 32);
-  const bool two = !quantize && !a.offsets && a.M > 8;
+  // (bf16 rows always come in groups, a few each.)
   cudaError_t r;
   if (quantize) r = launch_pdl(few_rows_kernel<true, 1, 1, true>, grid, block, 0, s, p);
-  else if (a.f8) r = two ? launch_pdl(few_rows_kernel<true, 2, 2, false>, grid, block, 0, s, p)
-                         : launch_pdl(few_rows_kernel<true, 1, 1, false>, grid, block, 0, s, p);
-  else r = two ? launch_pdl(few_rows_kernel<false, 2, 2, false>, grid, block, 0, s, p)
-               : launch_pdl(few_rows_kernel<false, 1, 4, false>, grid, block, 0, s, p);
+  else if (!a.f8) r = launch_pdl(few_rows_kernel<false, 1, 4, false>, grid, block, 0, s, p);
+  else if (!a.offsets && a.M > 8) r = launch_pdl(few_rows_kernel<true, 2, 2, false>, grid, block, 0, s, p);
+  else r = launch_pdl(few_rows_kernel<true, 1, 1, false>, grid, block, 0, s, p);
   return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);
 }
 

@@ -823,8 +823,8 @@ qlora_status launch_cfg(const ExpertArgs& a, cudaStream_t s, int split = 1) {
 
   const int64_t num_tiles = dw ? a.E * p.tiles_r * p.tiles_n : most_row_tiles(a, C::BM) * p.tiles_n;
   if (num_tiles > (int64_t(1) << 30)) return QLORA_ERR_SHAPE;
-  const int units = int(std::min<int64_t>(num_tiles, max_units));
-  if (C::SPLIT && num_tiles * split > max_units) return QLORA_ERR_SHAPE;   // one tile a cluster
+  // (SPLIT: one tile a cluster, however many run at once.)
+  const int units = int(C::SPLIT ? num_tiles : std::min<int64_t>(num_tiles, max_units));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -17,9 +17,9 @@ constexpr int kRowThreads = 256, kRowIlp = 4;
 // WHOLE: in % 128 == 0, so that block b starts at value 128 b (else a 64-bit division a block,
 // which cost a third of the time: 30 us for 8192 x 4096 against 22).
 template <bool WHOLE>
-__global__ void __launch_bounds__(kRowThreads) quantize_rows8_kernel(const uint16_t* __restrict__ X, int64_t blocks,
-                                                                     int64_t in, int64_t nb, uint8_t* __restrict__ codes,
-                                                                     float* __restrict__ scale) {
+__global__ void __launch_bounds__(kRowThreads) quantize_rows8_kernel(const uint16_t* X, int64_t blocks,
+                                                                     int64_t in, int64_t nb, uint8_t* codes,
+                                                                     float* scale) {
   pdl_wait();
   pdl_launch();
   const int sub = threadIdx.x & 15;
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows8_kernel(const uint1
         const int64_t col = (b - row * nb) * 128 + sub * 8;
         if (col < in) at[j] = row * in + col;
       }
-      if (at[j] >= 0) v[j] = __ldg(reinterpret_cast<const uint4*>(X + at[j]));
+      if (at[j] >= 0) v[j] = ld_global(reinterpret_cast<const uint4*>(X + at[j]));
     }
   }
 #pragma unroll
@@ -56,9 +56,9 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows8_kernel(const uint1
 // One CTA per 128 x 128 block, held in registers between the maximum and the codes:
 // thread t has the 8 columns 8 (t % 16).. of rows t / 16 + 16 j.
 template <bool F32>
-__global__ void __launch_bounds__(256) quantize_weight8_kernel(const void* __restrict__ W, int64_t out, int64_t in,
-                                                               int64_t nb_in, int64_t nb_out, uint8_t* __restrict__ codes,
-                                                               float* __restrict__ scale, int* status) {
+__global__ void __launch_bounds__(256) quantize_weight8_kernel(const void* W, int64_t out, int64_t in,
+                                                               int64_t nb_in, int64_t nb_out, uint8_t* codes,
+                                                               float* scale, int* status) {
   pdl_wait();
   pdl_launch();
   __shared__ uint32_t s_max[8];
@@ -78,11 +78,11 @@ __global__ void __launch_bounds__(256) quantize_weight8_kernel(const void* __res
     if (row < out && col < in) {
       if constexpr (F32) {
         const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(W) + base + row * in + col);
-        const float4 a = __ldg(src), b = __ldg(src + 1);
+        const float4 a = ld_global(src), b = ld_global(src + 1);
         f[j][0] = a.x; f[j][1] = a.y; f[j][2] = a.z; f[j][3] = a.w;
         f[j][4] = b.x; f[j][5] = b.y; f[j][6] = b.z; f[j][7] = b.w;
       } else {
-        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + base + row * in + col)),
+        bf16x8_to_f32(ld_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + base + row * in + col)),
                       f[j]);
       }
     }

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       bool bad = false;
       for (int i0 = 0; i0 <= p.E; i0 += 32) {
         const int i = i0 + int(lane);
-        const int raw = i <= p.E ? __ldg(p.offsets + i) : 0;
+        const int raw = i <= p.E ? ld_global(p.offsets + i) : 0;
         const int c = min(max(raw, 0), p.M);
         int v = max(c, run);
         for (int d = 1; d < 32; d <<= 1) {
@@ -502,22 +502,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int s = g % C::kScaleSlots;
           float a[2][4], w[C::kBlocksN][4];
           if (p.sa_vec) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(ra + k0));
-            const float4 v = __ldg(reinterpret_cast<const float4*>(rb + k0));
+            const float4 u = ld_global(reinterpret_cast<const float4*>(ra + k0));
+            const float4 v = ld_global(reinterpret_cast<const float4*>(rb + k0));
             a[0][0] = u.x; a[0][1] = u.y; a[0][2] = u.z; a[0][3] = u.w;
             a[1][0] = v.x; a[1][1] = v.y; a[1][2] = v.z; a[1][3] = v.w;
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              a[0][j] = __ldg(ra + min(k0 + j, x.nk - 1));
-              a[1][j] = __ldg(rb + min(k0 + j, x.nk - 1));
+              a[0][j] = ld_global(ra + min(k0 + j, x.nk - 1));
+              a[1][j] = ld_global(rb + min(k0 + j, x.nk - 1));
             }
           }
 #pragma unroll
           for (int b = 0; b < C::kBlocksN; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              w[b][j] = __ldg(sb + min((x.n0 >> 7) + b, p.nb_n - 1) * p.sb_n + min(k0 + j, x.nk - 1) * p.sb_k);
+              w[b][j] = ld_global(sb + min((x.n0 >> 7) + b, p.nb_n - 1) * p.sb_n + min(k0 + j, x.nk - 1) * p.sb_k);
           if (!__all_sync(0xffffffffu, mbar_wait_lazy(sempty_bar(s), ((g / C::kScaleSlots) & 1u) ^ 1u))) {
             if (lane == 0) set_status_site(p.status, QLORA_ERR_TIMEOUT, 66);
             ok = false;

@@ -65,16 +65,16 @@ __device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1,
 // 16 bytes at p and 16 at p + 64; zero where the row ends (at a multiple of 16; `left` from p).
 __device__ __forceinline__ void load32(uint32_t (&v)[8], const uint8_t* p, int left) {
   const uint4 z = make_uint4(0, 0, 0, 0);
-  const uint4 a = left >= 16 ? __ldg(reinterpret_cast<const uint4*>(p)) : z;
-  const uint4 b = left >= 80 ? __ldg(reinterpret_cast<const uint4*>(p) + 4) : z;
+  const uint4 a = left >= 16 ? ld_global(reinterpret_cast<const uint4*>(p)) : z;
+  const uint4 b = left >= 80 ? ld_global(reinterpret_cast<const uint4*>(p) + 4) : z;
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 // Weights are read once: not kept in L1.
 __device__ __forceinline__ void stream32(uint32_t (&v)[8], const uint8_t* p, int left) {
   const uint4 z = make_uint4(0, 0, 0, 0);
-  const uint4 a = left >= 16 ? __ldcs(reinterpret_cast<const uint4*>(p)) : z;
-  const uint4 b = left >= 80 ? __ldcs(reinterpret_cast<const uint4*>(p) + 4) : z;
+  const uint4 a = left >= 16 ? ld_stream(reinterpret_cast<const uint4*>(p)) : z;
+  const uint4 b = left >= 80 ? ld_stream(reinterpret_cast<const uint4*>(p) + 4) : z;
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
   int first = 0, last = p.M;
   if (p.offsets) {
     int v = 0;
-    for (int i = lane; i <= e; i += 32) v = max(v, __ldg(p.offsets + i));
-    const int r0 = __ldg(p.offsets + e), r1 = __ldg(p.offsets + e + 1);
+    for (int i = lane; i <= e; i += 32) v = max(v, ld_global(p.offsets + i));
+    const int r0 = ld_global(p.offsets + e), r1 = ld_global(p.offsets + e + 1);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
     first = min(v, p.M);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
 #pragma unroll
       for (int m = 0; m < kFewQuantRows; ++m)
         xv[m] = (m0 + m < last && col < p.in)
-                    ? __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.x) +
+                    ? ld_global(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.x) +
                                                            int64_t(m0 + m) * p.in + col))
                     : make_uint2(0, 0);
     };
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
               const int c = m0 + n * 8 + 2 * t + h;
               f[u][n][h] = 0.f;
               if (c < last && k < p.nk) {
-                if constexpr (QUANT) f[u][n][h] = xs[h] * __ldg(sb + k);
-                else f[u][n][h] = __ldg(p.sa + int64_t(c) * p.nk + k) * __ldg(sb + k);
+                if constexpr (QUANT) f[u][n][h] = xs[h] * ld_global(sb + k);
+                else f[u][n][h] = ld_global(p.sa + int64_t(c) * p.nk + k) * ld_global(sb + k);
               }
             }
           }

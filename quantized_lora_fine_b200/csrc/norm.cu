@@ -35,11 +35,11 @@ template <bool F32>
 __device__ __forceinline__ void load_w8(const void* w, int64_t col, float (&f)[8]) {
   if constexpr (F32) {
     const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(w) + col);
-    const float4 a = __ldg(src), b = __ldg(src + 1);
+    const float4 a = ld_global(src), b = ld_global(src + 1);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   } else {
-    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + col)), f);
+    bf16x8_to_f32(ld_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + col)), f);
   }
 }
 
@@ -63,8 +63,16 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 3 : 1) rms_norm_fwd_kernel(Nor
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int i = int(threadIdx.x) + j * T;
-    v[j] = i < nv ? __ldg(xr + i) : make_uint4(0, 0, 0, 0);
-    r[j] = (rr && i < nv) ? __ldg(rr + i) : make_uint4(0, 0, 0, 0);
+    v[j] = i < nv ? ld_global(xr + i) : make_uint4(0, 0, 0, 0);
+    r[j] = (rr && i < nv) ? ld_global(rr + i) : make_uint4(0, 0, 0, 0);
+  }
+  uint4 wv[VPT];
+  if constexpr (!WF32) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = int(threadIdx.x) + j * T;
+      wv[j] = i < nv ? ld_global(reinterpret_cast<const uint4*>(a.w) + i) : make_uint4(0, 0, 0, 0);
+    }
   }
   float ss = 0.f;
 #pragma unroll
@@ -83,14 +91,6 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 3 : 1) rms_norm_fwd_kernel(Nor
     for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
     const int i = int(threadIdx.x) + j * T;
     if (a.h && i < nv) reinterpret_cast<uint4*>(a.h + row * a.H)[i] = v[j];
-  }
-  uint4 wv[VPT];
-  if constexpr (!WF32) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int i = int(threadIdx.x) + j * T;
-      wv[j] = i < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + i) : make_uint4(0, 0, 0, 0);
-    }
   }
   ss = cta_sum(ss, s_part);
   const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ss, float(a.H)) + a.eps));
@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(NormBwd a) {
     for (int j = 0; j < VPT; ++j) {
       const int i = int(threadIdx.x) + j * T;
       const uint4 z = make_uint4(0, 0, 0, 0);
-      vy[j] = i < nv ? __ldg(reinterpret_cast<const uint4*>(a.dy + row * a.H) + i) : z;
-      vh[j] = i < nv ? __ldg(reinterpret_cast<const uint4*>(a.h + row * a.H) + i) : z;
-      vd[j] = (a.dh && i < nv) ? __ldg(reinterpret_cast<const uint4*>(a.dh + row * a.H) + i) : z;
+      vy[j] = i < nv ? ld_global(reinterpret_cast<const uint4*>(a.dy + row * a.H) + i) : z;
+      vh[j] = i < nv ? ld_global(reinterpret_cast<const uint4*>(a.h + row * a.H) + i) : z;
+      vd[j] = (a.dh && i < nv) ? ld_global(reinterpret_cast<const uint4*>(a.dh + row * a.H) + i) : z;
     }
-    const float rstd = __ldg(a.rstd + row);
+    const float rstd = ld_global(a.rstd + row);
     float c = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(NormBwd a) {
 }
 
 // dw[c] = the partial rows' sum: 32 columns x 32 row groups per CTA, groups added in order.
-__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restrict__ part, int rows, int H,
-                                                           float* __restrict__ dw) {
+__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* part, int rows, int H,
+                                                           float* dw) {
   __shared__ float s[32][33];
   pdl_wait();
   pdl_launch();

@@ -221,6 +221,19 @@ __device__ __forceinline__ void st_async_signal(uint32_t dst_cluster, uint32_t b
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A load of what the kernel before may have written, after pdl_wait(). (Not __ldg: its data has to
+// stay as it is for as long as the kernel is there, which is before pdl_wait() too, and the
+// compiler may move it up.)
+template <class T>
+__device__ __forceinline__ T ld_global(const T* p) { return *p; }
+// 16 bytes that are read once, not kept in L1 (volatile: stays behind pdl_wait()).
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // True in one lane of a converged warp. (The compiler knows that the code under it runs in one
 // lane, so the operands of tensor and copy instructions can stay in uniform registers.)
 __device__ __forceinline__ bool elect_one() {

@@ -152,6 +152,38 @@ def test_back_to_back_calls_do_not_overtake(cuda_device):
     assert torch.equal(chain(False), chain(True))
 
 
+@pytest.mark.parametrize("M", [1, 12, 300])
+def test_operands_written_by_the_call_before(cuda_device, M):
+    """Weights, scales, rows and norm weights that the call before writes, into memory that held others: as with
+    a wait after every call."""
+    Ws = [normal((2, 512, 512), i, 0.06).to(cuda_device) for i in range(6)]
+    off = torch.tensor([0, M // 3, M], dtype=torch.int32, device=cuda_device)
+    api.fp8_quantize_weight(Ws[0])
+
+    def chain(sync):
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        x = normal((M, 512), 9).to(cuda_device)
+        for W in Ws:
+            w = api.fp8_quantize_weight(W[0])
+            wait()
+            x = api.fp8_linear_fwd(w, x)
+            wait()
+            w = api.fp8_quantize_weight(W)
+            wait()
+            y = api.grouped_linear_fwd(w, x, off)
+            wait()
+            _, _, rstd = api.rms_norm_fwd(x, W[0, 0], EPS)
+            wait()
+            _, dw = api.rms_norm_bwd(y, x, rstd, W[0, 0])
+            wait()
+            x, _, _ = api.rms_norm_fwd(y, dw, EPS, residual=x)
+            wait()
+        return x
+
+    x = chain(True)
+    assert x.isfinite().all() and torch.equal(chain(False), x)
+
+
 def test_offsets_past_32_bits(cuda_device):
     """Rows, weights and outputs whose byte or element offsets pass 2^32."""
     dev = cuda_device

@@ -77,7 +77,7 @@ class Workspace:
                                    "call sets up the device's status word")
             buf = torch.zeros(256, dtype=torch.uint8, device=torch.device("cuda", index))
             torch.cuda.current_stream(index).synchronize()
-            cls._bufs[(index, None)] = buf
+            buf = cls._bufs.setdefault((index, None), buf)     # (another thread may have been first)
         return buf
 
     @classmethod
@@ -516,8 +516,6 @@ def _expert_weight(W, device: int) -> Tuple[_lib.ExpertWeight, int, int, int]:
         E, o, i = shape if len(shape) == 3 else (1, *shape)
         return _lib.ExpertWeight(E, o, i, 0, t.data_ptr(), W.scale.data_ptr(), None), E, o, i
     t, shape = W, W.shape
-    if len(shape) not in (2, 3):
-        raise ValueError("W must be [out, in] or [experts, out, in]")
     _check(t, _BF16, shape, "W", device)
     E, o, i = shape if len(shape) == 3 else (1, *shape)
     return _lib.ExpertWeight(E, o, i, 1, None, None, t.data_ptr()), E, o, i
@@ -646,6 +644,15 @@ def _output(t: Optional[torch.Tensor], shape: tuple, dtype, dev: int, name: str,
     return t
 
 
+def _sides(W) -> Tuple[int, int]:
+    """(out, in) of an FP8Weight or a bf16 tensor [(experts,) out, in]."""
+    if isinstance(W, FP8Weight):
+        return W.out, W.inp
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be [out, in] or [experts, out, in]")
+    return W.shape[-2:]
+
+
 def _parts(W) -> tuple:
     return (W.codes, W.scale) if isinstance(W, FP8Weight) else (W,)
 
@@ -702,7 +709,7 @@ def grouped_linear_fwd(W, X, offsets: torch.Tensor, Y: Optional[torch.Tensor] = 
     quantized first). offsets: int32 [experts + 1] on the device, ascending within 0 .. M; rows
     outside every group are not written (pass Y to keep what is in them)."""
     eight = isinstance(W, FP8Weight)
-    x, sx, dev = _rows_of(X, eight, W.inp if eight else W.shape[-1], "X")
+    x, sx, dev = _rows_of(X, eight, _sides(W)[1], "X")
     if _device() != dev:
         with torch.cuda.device(dev):
             return grouped_linear_fwd(W, X, offsets, Y)
@@ -729,7 +736,7 @@ def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, 
         raise ValueError("need_dX or need_dW must be true")
     if need_dW and eight:
         raise ValueError("an FP8Weight is frozen: pass need_dW=False")
-    d, sd, dev = _rows_of(dY, eight, W.out if eight else W.shape[-2], "dY")
+    d, sd, dev = _rows_of(dY, eight, _sides(W)[0], "dY")
     if _device() != dev:
         with torch.cuda.device(dev):
             return grouped_linear_bwd(W, X, dY, offsets, need_dX, need_dW, dX, dW)

@@ -139,6 +139,16 @@ def test_binding_refuses_cpu_tensors():
             call()
 
 
+@pytest.mark.parametrize("shape", [(), (16,), (1, 2, 16, 16)])
+def test_binding_refuses_weights_of_other_ranks(shape):
+    W, X = torch.zeros(shape, dtype=torch.bfloat16), torch.zeros(4, 16, dtype=torch.bfloat16)
+    off = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="experts, out, in"):
+        api.grouped_linear_fwd(W, X, off)
+    with pytest.raises(ValueError, match="experts, out, in"):
+        api.grouped_linear_bwd(W, X, X, off)
+
+
 def test_status_word_is_not_set_up_while_capturing(monkeypatch):
     """The first call on a device allocates the status word; under capture that is refused in words."""
     monkeypatch.setattr(api.Workspace, "_bufs", {})

@@ -1,16 +1,15 @@
 // Y_e = X_e W_e^T for few rows a group (decoding): bound by reading the weights once.
 //
-// A CTA takes 16 rows of one expert's weight over all of K, its 8 warps every eighth
-// 128-byte block of K. The rows stream from global memory into the registers of
+// A CTA takes 16 rows of one expert's weight over all of K, its 4, 8 or 16 warps every fourth,
+// eighth or sixteenth 128-byte block of K. The rows stream from global memory into the registers of
 // mma.sync fragments: lane (g, t) loads bytes 16 t .. and 64 + 16 t .. of weight rows g and
 // g + 8 and of token g, and gives their words to four products in the same order on both
 // sides (a sum over k may run over k in any order), so every load is 16 bytes wide, a warp's
 // cover whole sectors and nothing passes through shared memory. Weight rows are the
 // product's 16 rows, tokens its 8 columns. In e4m3 a block's product is scaled by sa sb and
 // added in fp32; the warps' sums are added in order at the end. 32 experts of 2048 x 4096, 31
-// of them with rows, 4 on average: bf16 84 us, 95 % of the copy bandwidth; e4m3, whose
-// products the hardware takes through 16-bit ones, 51 us, 77 %. (Weights by cp.async into
-// shared memory, 4 blocks ahead: 64 us.)
+// of them with rows, 4 on average: bf16 78 us, e4m3 48 (its products go through 16-bit ones).
+// (Weights by cp.async into shared memory, 4 blocks ahead: 64 us.)
 //
 // With bf16 rows and an e4m3 weight (QUANT, up to 2 rows in all) each warp quantizes the
 // blocks that it multiplies, as quantize_rows8_kernel does, which saves that launch (every
@@ -43,8 +42,6 @@ struct FewParams {
   int nk;                // 128-byte blocks of K
   int nb_n;              // scale rows per expert
 };
-
-constexpr int kFewWarps = 8;
 
 template <bool F8>
 __device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -79,13 +76,13 @@ __device__ __forceinline__ void stream32(uint32_t (&v)[8], const uint8_t* p, int
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// NT: 8-token columns a pass; U: blocks of K in flight a warp.
-template <bool F8, int NT, int U, bool QUANT>
-__global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_rows_kernel(const FewParams p) {
+// NT: 8-token columns a pass; U: blocks of K in flight a warp; WARPS a CTA, CTAS an SM.
+template <bool F8, int NT, int U, bool QUANT, int WARPS, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) few_rows_kernel(const FewParams p) {
   static_assert(kFewQuantRows == 2, "tokens 0 and 1 are lane t = 0's");
   static_assert(!QUANT || (F8 && NT == 1 && U == 1), "rows quantized here: kFewQuantRows, in e4m3");
-  __shared__ float red[kFewWarps][NT * 8][17];
-  __shared__ __align__(16) uint8_t xq[QUANT ? kFewWarps * kFewQuantRows * 128 : 16];
+  __shared__ float red[WARPS][NT * 8][17];
+  __shared__ __align__(16) uint8_t xq[QUANT ? WARPS * kFewQuantRows * 128 : 16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int e = blockIdx.y, n0 = blockIdx.x * 16;
@@ -125,12 +122,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
                     : make_uint2(0, 0);
     };
     if constexpr (QUANT) fetch(warp);
-    for (int k0 = warp; k0 < p.nk; k0 += kFewWarps * U) {
+    for (int k0 = warp; k0 < p.nk; k0 += WARPS * U) {
       uint32_t a[U][2][8], b[U][NT][8];
       float f[U][NT][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * kFewWarps;
+        const int k = k0 + u * WARPS;
         const int left = k < p.nk ? p.wbytes - k * 128 - 16 * t : 0;
         stream32(a[u][0], w0 + int64_t(k) * 128, left);
         stream32(a[u][1], w1 + int64_t(k) * 128, left);
@@ -142,7 +139,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
         uint2 v[kFewQuantRows];
 #pragma unroll
         for (int m = 0; m < kFewQuantRows; ++m) v[m] = xv[m];
-        fetch(k0 + kFewWarps);
+        fetch(k0 + WARPS);
         __syncwarp();
 #pragma unroll
         for (int m = 0; m < kFewQuantRows; ++m) {
@@ -162,7 +159,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * kFewWarps;
+        const int k = k0 + u * WARPS;
         const int left = k < p.nk ? p.wbytes - k * 128 - 16 * t : 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -217,11 +214,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[warp][n * 8 + 2 * t + (i & 1)][g + (i >> 1) * 8] = acc[n][i];
     __syncthreads();
-    const int r = threadIdx.x & 15, m = threadIdx.x >> 4;
-    if (m < NT * 8 && m0 + m < last) {
+    const int r = threadIdx.x & 15;
+    for (int m = threadIdx.x >> 4; m < NT * 8 && m0 + m < last; m += WARPS * 2) {
       float s = red[0][m][r];
 #pragma unroll
-      for (int k = 1; k < kFewWarps; ++k) s += red[k][m][r];
+      for (int k = 1; k < WARPS; ++k) s += red[k][m][r];
       p.y[int64_t(m0 + m) * p.out + n0 + r] = uint16_t(pack_bf16x2(s, s) & 0xFFFFu);
     }
     __syncthreads();
@@ -234,12 +231,21 @@ __global__ void __launch_bounds__(kFewWarps * 32, F8 && NT == 1 ? 4 : 2) few_row
 // but each pass fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 6.7 us against 16.6
 // with tiles; 64 experts of 1024 x 2048 in bf16: 32 us against 43 at one row a group, 48
 // against 48 at four, 80 against 50 at sixteen; in e4m3 18 against 25, and 32 against 30.
-// QLORA_B200_EXPERT_TILE set: never.
+// Every row in one group is the worst case: 128 rows in one of 32 experts of 2048 x 4096 in bf16
+// take 72 us, 19 with tiles. QLORA_B200_EXPERT_TILE set: never.
 bool few_rows_wanted(const ExpertArgs& a) {
   if (a.mode != ExpertMode::Fwd || std::getenv("QLORA_B200_EXPERT_TILE")) return false;
   return a.offsets ? a.M <= 4 * a.E : a.M <= 16;
 }
 
+// Warps a CTA: 4 where the CTAs are many, for the sums at the end and the first loads of small CTAs
+// overlap others' (64 experts of 1024 x 2048 at one and four rows a group: bf16 26 and 43 us, 8 warps
+// 32 and 48; e4m3 17 and 28, 8 warps 20 and 31); in e4m3 with 80 registers where they all run at once
+// (8 experts of 2048 x 2048 at four: 7.9 us, 12 with 64, which spill). More where there is no other CTA
+// to overlap with: 16 in e4m3 (4096 x 4096 5.6 us, 8 warps 6.4; 4096 x 11008 11.5 and 13.9; 2048 x 16384
+// 11.4 and 17; 11008 x 4096, 688 CTAs, 12.3 and 12.4), 8 in bf16 (one group of 4096 x 4096: 6.0 us, 4 warps
+// 7.1). Two passes in one (9 to 16 rows): 16 warps where each CTA has an SM (2048 x 16384: 14 us, 8
+// warps 18.6; 4096 x 4096, which has more CTAs: 9.4 and 7.7).
 qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s) {
   FewParams p = {};
   p.w = static_cast<const uint8_t*>(a.b);
@@ -256,13 +262,24 @@ qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s)
   p.wbytes = int(a.in) * (a.f8 ? 1 : 2);
   p.nk = (p.wbytes + 127) / 128;
   p.nb_n = int((a.out + 127) / 128);
-  const dim3 grid(unsigned(a.out / 16), unsigned(a.E)), block(kFewWarps * 32);
-  // (bf16 rows always come in groups, a few each.)
+  const dim3 grid(unsigned(a.out / 16), unsigned(a.E));
+  const int64_t ctas = int64_t(grid.x) * grid.y;
+  auto launch = [&](auto* kernel, int warps) { return launch_pdl(kernel, grid, dim3(unsigned(warps * 32)), 0, s, p); };
   cudaError_t r;
-  if (quantize) r = launch_pdl(few_rows_kernel<true, 1, 1, true>, grid, block, 0, s, p);
-  else if (!a.f8) r = launch_pdl(few_rows_kernel<false, 1, 4, false>, grid, block, 0, s, p);
-  else if (!a.offsets && a.M > 8) r = launch_pdl(few_rows_kernel<true, 2, 2, false>, grid, block, 0, s, p);
-  else r = launch_pdl(few_rows_kernel<true, 1, 1, false>, grid, block, 0, s, p);
+  if (quantize) {
+    r = launch(few_rows_kernel<true, 1, 1, true, 16, 2>, 16);
+  } else if (!a.f8) {   // (bf16 rows always come in groups, a few each)
+    r = ctas <= 148 * 2 ? launch(few_rows_kernel<false, 1, 4, false, 8, 2>, 8)
+                        : launch(few_rows_kernel<false, 1, 4, false, 4, 4>, 4);
+  } else if (!a.offsets && a.M > 8) {
+    r = ctas <= 148 ? launch(few_rows_kernel<true, 2, 1, false, 16, 1>, 16)
+                    : launch(few_rows_kernel<true, 2, 2, false, 8, 2>, 8);
+  } else if (!a.offsets || ctas <= 148 * 2) {
+    r = launch(few_rows_kernel<true, 1, 1, false, 16, 2>, 16);
+  } else {
+    r = ctas <= 148 * 8 ? launch(few_rows_kernel<true, 1, 1, false, 4, 6>, 4)
+                        : launch(few_rows_kernel<true, 1, 1, false, 4, 8>, 4);
+  }
   return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);
 }
 

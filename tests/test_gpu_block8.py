@@ -119,6 +119,13 @@ def test_linear_larger(cuda_device, M, o, i):
     _linear(cuda_device, M, o, i)
 
 
+@pytest.mark.parametrize("M", [1, 8, 9, 16])
+@pytest.mark.parametrize("o,i", [(2384, 2064), (4816, 1040)])
+def test_linear_few_rows(cuda_device, M, o, i):
+    """More blocks of 16 weight rows than SMs, and than SMs hold at once."""
+    _linear(cuda_device, M, o, i)
+
+
 @pytest.mark.parametrize("M", [17, 100, 130, 500])
 @pytest.mark.parametrize("o,i", [(144, 4112), (4112, 144), (1040, 2048), (16, 11008), (2176, 2560)])
 def test_linear_split_over_k(cuda_device, M, o, i):

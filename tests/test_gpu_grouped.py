@@ -88,6 +88,13 @@ def test_few_rows_a_group(cuda_device, sizes, kind):
     _run(cuda_device, sizes, 272, 1360, kind, before=0, after=0)
 
 
+@pytest.mark.parametrize("o", [32, 1360, 2576])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_few_rows_of_few_and_many_ctas(cuda_device, o, kind):
+    """16, 680 and 1288 blocks of 16 weight rows: each has its number of warps."""
+    _run(cuda_device, [2, 1, 0, 18, 1, 1, 0, 9], o, 1104, kind)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("sizes", [[30, 0, 130], [0, 0, 40], [200], [1, 33, 15, 0, 40]])
 @pytest.mark.parametrize("o,i", [(144, 4112), (2576, 272)])

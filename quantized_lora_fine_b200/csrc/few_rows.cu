@@ -227,15 +227,16 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) few_rows_kernel(const FewPar
 
 }  // namespace
 
-// Up to 16 rows of one group, or 4 a group on average (more rows are right, pass by pass,
-// but each pass fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 6.7 us against 16.6
-// with tiles; 64 experts of 1024 x 2048 in bf16: 32 us against 43 at one row a group, 48
-// against 48 at four, 80 against 50 at sixteen; in e4m3 18 against 25, and 32 against 30.
-// Every row in one group is the worst case: 128 rows in one of 32 experts of 2048 x 4096 in bf16
-// take 72 us, 19 with tiles. QLORA_B200_EXPERT_TILE set: never.
+// Up to 16 rows of one group, or 4 a group on average, 5 in bf16 (more rows are right, pass by
+// pass, but each pass fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 6.7 us against 16.6
+// with tiles. 64 experts of 1024 x 2048 at four, five and eight rows a group: bf16 43, 44 and 53 us, tiles
+// 47, 47 and 48; e4m3 28, 29 and 35, tiles 29, 29 and 30; 16 of 5120 x 5120: bf16 122, 129 and 163, tiles
+// 142, 144 and 145; e4m3 74, 76 and 99, tiles 77, 79 and 79. Every row in one group is the worst case: 128
+// rows in one of 32 experts of 2048 x 4096 in bf16 take 72 us, 19 with tiles.
+// QLORA_B200_EXPERT_TILE set: never.
 bool few_rows_wanted(const ExpertArgs& a) {
   if (a.mode != ExpertMode::Fwd || std::getenv("QLORA_B200_EXPERT_TILE")) return false;
-  return a.offsets ? a.M <= 4 * a.E : a.M <= 16;
+  return a.offsets ? a.M <= (a.f8 ? 4 : 5) * a.E : a.M <= 16;
 }
 
 // Warps a CTA: 4 where the CTAs are many, for the sums at the end and the first loads of small CTAs

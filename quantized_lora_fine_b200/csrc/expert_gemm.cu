@@ -573,8 +573,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
           uint64_t v[32];
-          tmem_ld_32x32b_x64_pairs(trow + buf * C::BN + c * 64, v);
-          tmem_ld_wait_for(v);
+          tmem_ld_wait_32x32b_x64_pairs(trow + buf * C::BN + c * 64, v);
           if (c + 1 == kLoads) {
               tc_fence_before();
               __syncwarp();

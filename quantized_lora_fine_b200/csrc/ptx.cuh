@@ -321,11 +321,14 @@ __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 32 lanes x 64 consecutive columns as 32 pairs of neighbours (for packed arithmetic).
-__device__ __forceinline__ void tmem_ld_32x32b_x64_pairs(uint32_t taddr, uint64_t (&v)[32]) {
+// 32 lanes x 64 consecutive columns as 32 pairs of neighbours (for packed arithmetic), waited for: the
+// load's registers hold nothing defined before the wait, so the load, the wait and the moves that read
+// them are one statement.
+__device__ __forceinline__ void tmem_ld_wait_32x32b_x64_pairs(uint32_t taddr, uint64_t (&v)[32]) {
   asm volatile(
       "{\n\t.reg .b32 t<64>;\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31, t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47, t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
       "mov.b64 %0, {t0, t1};\n\t"
       "mov.b64 %1, {t2, t3};\n\t"
       "mov.b64 %2, {t4, t5};\n\t"
@@ -360,12 +363,8 @@ __device__ __forceinline__ void tmem_ld_32x32b_x64_pairs(uint32_t taddr, uint64_
       "mov.b64 %31, {t62, t63};\n\t"
       "}"
       : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15]), "=l"(v[16]), "=l"(v[17]), "=l"(v[18]), "=l"(v[19]), "=l"(v[20]), "=l"(v[21]), "=l"(v[22]), "=l"(v[23]), "=l"(v[24]), "=l"(v[25]), "=l"(v[26]), "=l"(v[27]), "=l"(v[28]), "=l"(v[29]), "=l"(v[30]), "=l"(v[31])
-      : "r"(taddr));
-}
-
-// The wait with the loaded registers as operands: no use of them can move before it.
-__device__ __forceinline__ void tmem_ld_wait_for(uint64_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+l"(v[0]), "+l"(v[1]), "+l"(v[2]), "+l"(v[3]), "+l"(v[4]), "+l"(v[5]), "+l"(v[6]), "+l"(v[7]), "+l"(v[8]), "+l"(v[9]), "+l"(v[10]), "+l"(v[11]), "+l"(v[12]), "+l"(v[13]), "+l"(v[14]), "+l"(v[15]), "+l"(v[16]), "+l"(v[17]), "+l"(v[18]), "+l"(v[19]), "+l"(v[20]), "+l"(v[21]), "+l"(v[22]), "+l"(v[23]), "+l"(v[24]), "+l"(v[25]), "+l"(v[26]), "+l"(v[27]), "+l"(v[28]), "+l"(v[29]), "+l"(v[30]), "+l"(v[31])::"memory");
+      : "r"(taddr)
+      : "memory");
 }
 
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading and

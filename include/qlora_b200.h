@@ -452,9 +452,12 @@ qlora_status nf4_layer_error_rank_noalloc(int32_t n_layers, const uint16_t* cons
  *
  * e4m3 blocks: a block's a = max(max|x|, 2^-100), scale = fp32(a / 448), codes
  * = e4m3 (OCP, 448 the largest) of the real quotient 448 x / a, nearest, ties to
- * even; the value a code stands for is code * scale. A block that holds a NaN or
- * an infinity gets NaN codes. Rows (activations, output gradients) have a scale
- * for each 1 x 128 block, [M][ceil(in / 128)]; weights for each 128 x 128 block,
+ * even, for bf16 rows and bf16 and fp32 weights; the norm's y, which is a rounded
+ * fp32 product itself, is coded by that quotient in fp32 (off by less than 2^-22 of
+ * itself: next to the midpoint of two codes either may come out). The value a code
+ * stands for is code * scale. A block that holds a NaN or an infinity gets NaN codes.
+ * Rows (activations, output gradients) have a scale for each 1 x 128 block,
+ * [M][ceil(in / 128)]; weights for each 128 x 128 block,
  * [experts][ceil(out / 128)][ceil(in / 128)]; the last blocks may be short.
  *
  * `in` and `out` are multiples of 16 up to 2^24, M is 1 .. 2^30, any value in

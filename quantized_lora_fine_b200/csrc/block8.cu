@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) quantize_weight8_kernel(const void* W, in
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t row = row0 + 16 * j;
-    if (row < out && col < in) *reinterpret_cast<uint2*>(codes + base + row * in + col) = quantize8(f[j], q);
+    if (row < out && col < in) *reinterpret_cast<uint2*>(codes + base + row * in + col) = quantize8<F32>(f[j], q);
   }
   if (threadIdx.x == 0) {
     scale[blk] = q.scale;

@@ -5,13 +5,22 @@
 //   q = e4m3_rne(448 x / a) of the real quotient.
 //
 // The quotient is decided in fp32: with p = 2^-exponent(a), a' = a p is in [1, 2) and
-// u = 448 p x (both exact for bf16 x: 8 + 3 significant bits), t = u y with y near 1 / a', and t is
-// corrected once by its remainder, t + (u - t a') y (Markstein's quotient step; the
-// remainder is exact, so y needs no more than a few last places). That returns the real
-// quotient wherever it is representable, so a quotient on the midpoint of two e4m3 values
-// is seen as the midpoint and rounds to even; no other quotient of two bf16 values is within
-// fp32 rounding of one. The scale is the same step with 448. A block that holds a NaN or an
-// infinity gets NaN codes: its p is infinite.
+// u = 448 p x, t = u y with y near 1 / a', and t is corrected once by its remainder,
+// t + (u - t a') y (Markstein's quotient step; the remainder is exact, so y needs no more than
+// a few last places).
+//   bf16 x: u is exact (8 + 3 significant bits) and t is the real quotient wherever that is
+// representable, so a quotient on the midpoint of two e4m3 values is seen as the midpoint and
+// rounds to even; no other quotient of two bf16 values is within fp32 rounding of one.
+//   fp32 weights: u is rounded too, t is up to two last places from the real quotient, and that may lie
+// so near to a midpoint m on either side (4 weights in 10^7 of a normal distribution came out a code
+// off): where t is within 8 places of an m, the sign of 448 p x - m a' decides (block8_decide).
+//   The norm's y: quantized by t. y is itself a rounded product, and real quotients on a midpoint are
+// common there (6 values in 10^4: h and w have 8 bits each); t's rounding returns most of them to
+// the midpoint that y's rounding left. Deciding by the exact quotient of the rounded y gave half as many
+// codes again that differ from those of the unrounded one (326 for 215 of 400 x 4096), and at 8192 x
+// 4096 took 50 us for 40.
+//   The scale is the same step with 448 (equal to the division for all 2^23 significands). A block that
+// holds a NaN or an infinity gets NaN codes: its p is infinite.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -92,10 +101,36 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {
   return m;
 }
 
+// The quotient of an fp32 x, or where it is within 8 places of a value m of 5 significant bits (as
+// midpoints are, all 2^-10 or more): m, if the real quotient is m, else m's neighbour on its side.
+// u + lo is 448 p x; u - m a' is exact, for the two agree in all but their last places; its sum with lo
+// has the real difference's sign.
+__device__ __forceinline__ float block8_decide(float x, const Block8& b) {
+  const float t = block8_quotient(x, b);
+  const uint32_t bits = __float_as_uint(t) & 0x7FFFFFFFu;
+  if (((bits + 8u) & 0x7FFFFu) >= 16u || bits - 0x3A000000u >= 0x0A000000u) return t;   // (2^-11 .. 2^9)
+  const uint32_t m = (bits + 8u) & ~0x7FFFFu, sign = __float_as_uint(x) & 0x80000000u;
+  const float u = __fmul_rn(x, b.c), lo = __fmaf_rn(x, b.c, -u);
+  const float d = __fadd_rn(__fmaf_rn(-__uint_as_float(m | sign), b.a, u), lo);
+  const bool in = (__float_as_uint(d) & 0x80000000u) != sign;      // towards zero
+  return __uint_as_float((d == 0.f ? m : in ? m - 1u : m + 1u) | sign);
+}
+
+// EXACT: codes of the real quotients of fp32 values. (Few threads meet a value that needs it.)
+template <bool EXACT = false>
 __device__ __forceinline__ uint2 quantize8(const float (&f)[8], const Block8& b) {
   float q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = block8_quotient(f[i], b);
+  if constexpr (EXACT) {
+    uint32_t off = 0x7FFFFu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) off = min(off, (__float_as_uint(q[i]) + 8u) & 0x7FFFFu);
+    if (off < 16u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = block8_decide(f[i], b);
+    }
+  }
   return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
 

@@ -7,9 +7,16 @@
 // sides (a sum over k may run over k in any order), so every load is 16 bytes wide, a warp's
 // cover whole sectors and nothing passes through shared memory. Weight rows are the
 // product's 16 rows, tokens its 8 columns. In e4m3 a block's product is scaled by sa sb and
-// added in fp32; the warps' sums are added in order at the end. 32 experts of 2048 x 4096, 31
-// of them with rows, 4 on average: bf16 78 us, e4m3 48 (its products go through 16-bit ones).
-// (Weights by cp.async into shared memory, 4 blocks ahead: 64 us.)
+// added in fp32; the warps' sums are added in order at the end. 32 experts of 2048 x 4096, 4 rows
+// on average: bf16 81 us, e4m3 45 (its products go through 16-bit ones).
+// (e4m3 weights by cp.async into shared memory, 4 blocks ahead: 64 us for 51 then.)
+//
+// A CTA makes one pass of 8 rows over its own expert's weight rows. Groups with more rows have later
+// passes; they are one list, dealt out to the first CTAs, one each, so that no CTA makes more than two
+// passes however the rows are routed. (An expert's own CTAs for all of its passes: with all rows in
+// one of 32 experts of 2048 x 4096, 128 rows took 115 us in bf16 and 79 in e4m3 for 35 and 22; in one of 1024 of
+// 256 x 256, 4096 rows took 438 and 362 for 75 and 50. Evenly routed: 84 and 48 us for 84 and 47, and 61
+// and 34 for 66 and 35.)
 //
 // With bf16 rows and an e4m3 weight (QUANT, up to 2 rows in all) each warp quantizes the
 // blocks that it multiplies, as quantize_rows8_kernel does, which saves that launch (every
@@ -76,36 +83,128 @@ __device__ __forceinline__ void stream32(uint32_t (&v)[8], const uint8_t* p, int
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// NT: 8-token columns a pass; U: blocks of K in flight a warp; WARPS a CTA, CTAS an SM.
-template <bool F8, int NT, int U, bool QUANT, int WARPS, int CTAS>
+// Pass `y` of the list of all groups' passes but their first, ROWS rows each (a group's last has what is
+// left), found by the whole warp, 128 groups at a time, four a lane: its expert, its first row and the end
+// of its group. False past the list's end.
+template <int ROWS>
+__device__ __forceinline__ bool later_pass(const FewParams& p, int y, int lane, int& e, int& m0, int& last) {
+  int run = 0, before = 0;                        // the running maximum, and the passes, of the groups so far
+  for (int c = 0; c < p.E; c += 128) {
+    const int b = c + lane * 4;
+    int s[5];                                     // starts of the lane's groups and the last one's end
+#pragma unroll
+    for (int j = 0; j < 5; ++j) s[j] = min(max(ld_global(p.offsets + min(b + j, p.E)), 0), p.M);
+    int top = max(max(s[0], s[1]), max(s[2], s[3]));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, top, d);
+      if (lane >= d) top = max(top, u);
+    }
+    const int left = __shfl_up_sync(0xffffffffu, top, 1);
+    s[0] = max(s[0], lane == 0 ? run : max(run, left));
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[j + 1] = max(s[j], s[j + 1]);
+      n += max(s[j + 1] - s[j] - 1, 0) / ROWS;
+    }
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += u;
+    }
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
+    if (y < before + all) {
+      int k = y - before - (upto - n);            // in 0 .. n - 1 for the lane that has it
+      const uint32_t who = __ballot_sync(0xffffffffu, k >= 0 && k < n);
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int of = max(s[j + 1] - s[j] - 1, 0) / ROWS;
+        if (!found && k < of) {
+          found = true;
+          e = b + j;
+          m0 = s[j] + (k + 1) * ROWS;
+          last = s[j + 1];
+        }
+        k -= of;
+      }
+      const int src = __ffs(int(who)) - 1;
+      e = __shfl_sync(0xffffffffu, e, src);
+      m0 = __shfl_sync(0xffffffffu, m0, src);
+      last = __shfl_sync(0xffffffffu, last, src);
+      return true;
+    }
+    before += all;
+    run = max(run, __shfl_sync(0xffffffffu, top, 31));
+  }
+  return false;
+}
+
+// NT: 8-token columns a pass; U: blocks of K in flight a warp; WARPS a CTA, CTAS an SM. GROUPS: rows by
+// offsets; else all rows (one pass) go through one weight.
+template <bool F8, int NT, int U, bool GROUPS, bool QUANT, int WARPS, int CTAS>
 __global__ void __launch_bounds__(WARPS * 32, CTAS) few_rows_kernel(const FewParams p) {
   static_assert(kFewQuantRows == 2, "tokens 0 and 1 are lane t = 0's");
-  static_assert(!QUANT || (F8 && NT == 1 && U == 1), "rows quantized here: kFewQuantRows, in e4m3");
+  static_assert(!QUANT || (F8 && NT == 1 && U == 1 && !GROUPS), "rows quantized here: kFewQuantRows, in e4m3");
   __shared__ float red[WARPS][NT * 8][17];
+  __shared__ int s_later[WARPS];
   __shared__ __align__(16) uint8_t xq[QUANT ? WARPS * kFewQuantRows * 128 : 16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int e = blockIdx.y, n0 = blockIdx.x * 16;
+  constexpr int ROWS = NT * 8;
+  const int n0 = blockIdx.x * 16;
+  int e = blockIdx.y;
   pdl_wait();
   pdl_launch();
   // The group's rows: the running maximum of the offsets clamped to [0, M], as the tiled kernel.
-  int first = 0, last = p.M;
-  if (p.offsets) {
+  int m0 = 0, last = p.M;
+  // Passes beyond their groups' first go to the first CTAs, one each: there are (M - 1) / ROWS at most.
+  const bool helps = GROUPS && int(blockIdx.y) < (p.M - 1) / ROWS;
+  if constexpr (GROUPS) {
+    const int i0 = helps ? int(threadIdx.x) : p.E;
+    const int o0 = i0 < p.E ? ld_global(p.offsets + i0) : 0, o1 = i0 < p.E ? ld_global(p.offsets + i0 + 1) : 0;
     int v = 0;
     for (int i = lane; i <= e; i += 32) v = max(v, ld_global(p.offsets + i));
     const int r0 = ld_global(p.offsets + e), r1 = ld_global(p.offsets + e + 1);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
-    first = min(v, p.M);
-    last = max(first, min(max(r1, 0), p.M));
+    m0 = min(v, p.M);
+    last = max(m0, min(max(r1, 0), p.M));
     if (blockIdx.x == 0 && threadIdx.x == 0 && (r0 < 0 || r1 > p.M || r1 < r0))
       set_status_site(p.status, QLORA_ERR_SHAPE, 70);
+    if (helps) {                                   // how many (at least as many where the offsets descend)
+      auto beyond = [&](int from, int to) {
+        return max(min(max(to, 0), p.M) - min(max(from, 0), p.M) - 1, 0) / ROWS;
+      };
+      int n = beyond(o0, o1);
+      for (int i = i0 + WARPS * 32; i < p.E; i += WARPS * 32)
+        n += beyond(ld_global(p.offsets + i), ld_global(p.offsets + i + 1));
+      n = int(__reduce_add_sync(0xffffffffu, unsigned(n)));
+      if (lane == 0) s_later[warp] = n;
+    }
   }
-  const uint8_t* w0 = p.w + (int64_t(e) * p.out + n0 + g) * p.wbytes + 16 * t;
-  const uint8_t* w1 = w0 + int64_t(8) * p.wbytes;
-  const float* sb = F8 ? p.sb + (int64_t(e) * p.nb_n + (n0 >> 7)) * p.nk : nullptr;
-
-  for (int m0 = first; m0 < last; m0 += NT * 8) {
+  // After a barrier: the next of the groups' later passes for this CTA, if there is one. (A group that has most of
+  // the rows would keep its own CTAs for a pass after another.)
+  int y = blockIdx.y;
+  auto next = [&]() {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) n += s_later[i];
+    if (y >= n || !later_pass<ROWS>(p, y, lane, e, m0, last)) return false;
+    y += gridDim.y;
+    return true;
+  };
+  if (GROUPS && m0 >= last) {
+    if (!helps) return;
+    __syncthreads();
+    if (!next()) return;
+  }
+  for (;;) {
+    const uint8_t* w0 = p.w + (int64_t(e) * p.out + n0 + g) * p.wbytes + 16 * t;
+    const uint8_t* w1 = w0 + int64_t(8) * p.wbytes;
+    const float* sb = F8 ? p.sb + (int64_t(e) * p.nb_n + (n0 >> 7)) * p.nk : nullptr;
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -215,25 +314,27 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) few_rows_kernel(const FewPar
       for (int i = 0; i < 4; ++i) red[warp][n * 8 + 2 * t + (i & 1)][g + (i >> 1) * 8] = acc[n][i];
     __syncthreads();
     const int r = threadIdx.x & 15;
-    for (int m = threadIdx.x >> 4; m < NT * 8 && m0 + m < last; m += WARPS * 2) {
+    for (int m = threadIdx.x >> 4; m < ROWS && m0 + m < last; m += WARPS * 2) {
       float s = red[0][m][r];
 #pragma unroll
       for (int k = 1; k < WARPS; ++k) s += red[k][m][r];
       p.y[int64_t(m0 + m) * p.out + n0 + r] = uint16_t(pack_bf16x2(s, s) & 0xFFFFu);
     }
+    if (!helps || !next()) return;
     __syncthreads();
   }
 }
 
 }  // namespace
 
-// Up to 16 rows of one group, or 4 a group on average, 5 in bf16 (more rows are right, pass by
-// pass, but each pass fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 6.7 us against 16.6
-// with tiles. 64 experts of 1024 x 2048 at four, five and eight rows a group: bf16 43, 44 and 53 us, tiles
+// Up to 16 rows of one group, or 4 a group on average, 5 in bf16 (more rows are right, but each pass of 8
+// fetches the weights again). 4096 x 4096 in e4m3 at 16 rows: 7.4 us against 9.6 with tiles (4096 x 11008:
+// 15.7 and 14.8). 64 experts of 1024 x 2048 at four, five and eight rows a group: bf16 43, 44 and 53 us, tiles
 // 47, 47 and 48; e4m3 28, 29 and 35, tiles 29, 29 and 30; 16 of 5120 x 5120: bf16 122, 129 and 163, tiles
-// 142, 144 and 145; e4m3 74, 76 and 99, tiles 77, 79 and 79. Every row in one group is the worst case: 128
-// rows in one of 32 experts of 2048 x 4096 in bf16 take 72 us, 19 with tiles.
-// QLORA_B200_EXPERT_TILE set: never.
+// 142, 144 and 145; e4m3 74, 76 and 99, tiles 77, 79 and 79. With every row in one group a call takes no longer
+// than with even groups, but tiles take less: 128 rows in one of 32 experts of 2048 x 4096, 35 us in bf16 and
+// 22 in e4m3, tiles 20 and 14; 1024 in one of 256 of 768 x 2048, 64 and 45, tiles 19 and 16. The host does not see
+// the groups' sizes. QLORA_B200_EXPERT_TILE set: never.
 bool few_rows_wanted(const ExpertArgs& a) {
   if (a.mode != ExpertMode::Fwd || std::getenv("QLORA_B200_EXPERT_TILE")) return false;
   return a.offsets ? a.M <= (a.f8 ? 4 : 5) * a.E : a.M <= 16;
@@ -268,18 +369,20 @@ qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s)
   auto launch = [&](auto* kernel, int warps) { return launch_pdl(kernel, grid, dim3(unsigned(warps * 32)), 0, s, p); };
   cudaError_t r;
   if (quantize) {
-    r = launch(few_rows_kernel<true, 1, 1, true, 16, 2>, 16);
+    r = launch(few_rows_kernel<true, 1, 1, false, true, 16, 2>, 16);
   } else if (!a.f8) {   // (bf16 rows always come in groups, a few each)
-    r = ctas <= 148 * 2 ? launch(few_rows_kernel<false, 1, 4, false, 8, 2>, 8)
-                        : launch(few_rows_kernel<false, 1, 4, false, 4, 4>, 4);
+    r = ctas <= 148 * 2 ? launch(few_rows_kernel<false, 1, 4, true, false, 8, 2>, 8)
+                        : launch(few_rows_kernel<false, 1, 4, true, false, 4, 4>, 4);
   } else if (!a.offsets && a.M > 8) {
-    r = ctas <= 148 ? launch(few_rows_kernel<true, 2, 1, false, 16, 1>, 16)
-                    : launch(few_rows_kernel<true, 2, 2, false, 8, 2>, 8);
-  } else if (!a.offsets || ctas <= 148 * 2) {
-    r = launch(few_rows_kernel<true, 1, 1, false, 16, 2>, 16);
+    r = ctas <= 148 ? launch(few_rows_kernel<true, 2, 1, false, false, 16, 1>, 16)
+                    : launch(few_rows_kernel<true, 2, 2, false, false, 8, 2>, 8);
+  } else if (!a.offsets) {
+    r = launch(few_rows_kernel<true, 1, 1, false, false, 16, 2>, 16);
+  } else if (ctas <= 148 * 2) {
+    r = launch(few_rows_kernel<true, 1, 1, true, false, 16, 2>, 16);
   } else {
-    r = ctas <= 148 * 8 ? launch(few_rows_kernel<true, 1, 1, false, 4, 6>, 4)
-                        : launch(few_rows_kernel<true, 1, 1, false, 4, 8>, 4);
+    r = ctas <= 148 * 8 ? launch(few_rows_kernel<true, 1, 1, true, false, 4, 6>, 4)
+                        : launch(few_rows_kernel<true, 1, 1, true, false, 4, 8>, 4);
   }
   return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);
 }

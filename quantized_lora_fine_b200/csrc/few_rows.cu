@@ -342,12 +342,11 @@ bool few_rows_wanted(const ExpertArgs& a) {
 
 // Warps a CTA: 4 where the CTAs are many, for the sums at the end and the first loads of small CTAs
 // overlap others' (64 experts of 1024 x 2048 at one and four rows a group: bf16 26 and 43 us, 8 warps
-// 32 and 48; e4m3 17 and 28, 8 warps 20 and 31); in e4m3 with 80 registers where they all run at once
-// (8 experts of 2048 x 2048 at four: 7.9 us, 12 with 64, which spill). More where there is no other CTA
-// to overlap with: 16 in e4m3 (4096 x 4096 5.6 us, 8 warps 6.4; 4096 x 11008 11.5 and 13.9; 2048 x 16384
-// 11.4 and 17; 11008 x 4096, 688 CTAs, 12.3 and 12.4), 8 in bf16 (one group of 4096 x 4096: 6.0 us, 4 warps
-// 7.1). Two passes in one (9 to 16 rows): 16 warps where each CTA has an SM (2048 x 16384: 14 us, 8
-// warps 18.6; 4096 x 4096, which has more CTAs: 9.4 and 7.7).
+// 32 and 48; e4m3 17 and 28, 8 warps 20 and 31). More where there is no other CTA to overlap with: 16 in e4m3
+// (4096 x 4096 5.3 us, 8 warps 6.2; 4096 x 11008 10.5 and 13.3; 2048 x 16384 11.4 and 16.9; 11008 x 4096, 688
+// CTAs, 11.2 and 11.4), 8 in bf16 (one group of 4096 x 4096: 6.0 us, 4 warps 7.1). Two passes in one
+// (9 to 16 rows): 16 warps where each CTA has an SM (2048 x 16384: 14 us, 8 warps 18.6; 4096 x 4096, which has
+// more CTAs: 9.4 and 7.7).
 qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s) {
   FewParams p = {};
   p.w = static_cast<const uint8_t*>(a.b);
@@ -381,8 +380,7 @@ qlora_status launch_few_rows(const ExpertArgs& a, bool quantize, cudaStream_t s)
   } else if (ctas <= 148 * 2) {
     r = launch(few_rows_kernel<true, 1, 1, true, false, 16, 2>, 16);
   } else {
-    r = ctas <= 148 * 8 ? launch(few_rows_kernel<true, 1, 1, true, false, 4, 6>, 4)
-                        : launch(few_rows_kernel<true, 1, 1, true, false, 4, 8>, 4);
+    r = launch(few_rows_kernel<true, 1, 1, true, false, 4, 8>, 4);
   }
   return r == cudaSuccess ? QLORA_OK : (cudaGetLastError(), QLORA_ERR_CUDA);
 }

@@ -754,7 +754,7 @@ def grouped_linear_bwd(W, X: Optional[torch.Tensor], dY, offsets: torch.Tensor, 
         d, sd = q.codes, q.scale
     ws = _status_ptr(dev)
     dX = _output(dX, (M, i), _BF16, dev, "dX", d, sd, *_parts(W), offsets, X if need_dW else None) if need_dX else None
-    dW = _output(dW, (E, o, i), _F32, dev, "dW", d, X, offsets, dX) if need_dW else None
+    dW = _output(dW, (E, o, i), _F32, dev, "dW", d, X, *_parts(W), offsets, dX) if need_dW else None
     check(_lib.load().qlora_grouped_linear_bwd(ctypes.byref(cs), xp, d.data_ptr(), _ptr(sd), M, offsets.data_ptr(),
                                                _ptr(dX), _ptr(dW), ws, 256, _raw_stream(dev)),
           "qlora_grouped_linear_bwd")

@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows8_kernel(const uint1
 }
 
 // One CTA per 128 x 128 block, held in registers between the maximum and the codes:
-// thread t has the 8 columns 8 (t % 16).. of rows t / 16 + 16 j.
+// thread t has the 8 columns 8 (t % 16).. of rows t / 16 + 16 j. 4096 x 4096: bf16 13.9 us, fp32 18.4 (the bytes
+// take 7.7 and 12.8); two CTAs an SM and a barrier in each, so neither memory nor issue slots are full.
 template <bool F32>
 __global__ void __launch_bounds__(256) quantize_weight8_kernel(const void* W, int64_t out, int64_t in,
                                                                int64_t nb_in, int64_t nb_out, uint8_t* codes,

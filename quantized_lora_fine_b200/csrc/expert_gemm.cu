@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int n = min(4, x.nk - k);
           // Four in a row without a loop between them where the registers last: at 2048 rows,
           // 4096 x 4096, 40.5 us in 128 x 128 tiles against 48.5 (53 with the tests of each step in
-          // the loop); 256-column tiles would spill (61 us against 40).
+          // the loop); 256-column tiles would spill (61 us against 40). (With K split 24 bytes a thread spill.)
           if (!C::WIDE && n == 4) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) take(lds_f32(f + j * C::kBlocksN * 512));
@@ -764,7 +764,9 @@ int resident_units() {
   return n;
 }
 
-// K steps of each CTA of a cluster that splits nk of them (whole groups of four scales).
+// K steps of each CTA of a cluster that splits nk of them, in whole groups of four (e4m3's scales come
+// four steps at a time): shares are rounded up, so the last CTAs may have fewer steps or none (33 steps
+// over 4: 12, 12, 9, 0), and those without send zeros.
 int split_part(int nk, int split) { return ((nk + split - 1) / split + 3) / 4 * 4; }
 
 // Row tiles at most: every group may end inside a tile.
@@ -893,7 +895,7 @@ ExpertTileKind tile_kind(const ExpertArgs& a) {
 }
 
 // CTAs that share a 128 x 128 tile's K: where even the most tiles that there can be leave SMs
-// idle, each CTA keeps eight steps, and all clusters run at once (16 of 8 CTAs do not: 22.9 us
+// idle, a share is eight steps or more, and all clusters run at once (16 of 8 CTAs do not: 22.9 us
 // where 16 of 4 took 16.9, e4m3 at 256 rows, 1024 x 11008). e4m3 at 64 rows, 4096 x 4096: 9.7 us by four CTAs,
 // 14.7 by one; 4096 x 11008: 17.1 and 35; at 256 rows by two: 13.4 and 15.9. bf16 at 17 rows,
 // 4096 x 4096: 10.1 by four.

@@ -468,7 +468,8 @@ qlora_status nf4_layer_error_rank_noalloc(int32_t n_layers, const uint16_t* cons
 /* h = bf16(x + residual) (x where residual is NULL; h may be NULL then),
  * rstd = 1 / sqrt(mean(h^2) + eps) per row (fp32 [M]), y = h rstd weight, as bf16
  * (y), as e4m3 codes with scales (y_codes, y_scale; quantized from the fp32
- * value), or both; at least one. weight: bf16 or fp32 [H]. H % 8 == 0, H <= 32768.
+ * value), or both; at least one. The sum of squares is fp32: a row whose squares add
+ * up past 2^128 has rstd 0. weight: bf16 or fp32 [H]. H % 8 == 0, H <= 32768.
  * h may be x or residual itself. */
 qlora_status qlora_rms_norm_fwd(const uint16_t* x, const uint16_t* residual, const void* weight, int32_t w_dtype,
                                 int64_t M, int64_t H, float eps, uint16_t* h, uint16_t* y, uint8_t* y_codes,

@@ -7,8 +7,8 @@
 // the fp32 value, one rounding), or both. Sums, rstd and dw are fp32. Both directions
 // are bound by memory: a row stays in registers between its sum and its output (in the backward up to
 // H = 16384; above, 450 bytes a thread spill: with dw 1024 x 32768 takes 105 us, 2048 x 16384 64, 4096 x
-// 8192 47). Rows under 512 values leave lanes of their CTA idle: 131072 x 128 takes 137 us forward, 4096 x
-// 8192, as many values, 28.
+// 8192 47). Each row is a CTA forward, of 32 threads at least: 131072 rows of 128 take 137 us, 4096 x 8192
+// with twice the values 28.
 #include <algorithm>
 
 #include "internal.cuh"
